@@ -32,7 +32,8 @@ int check_launch(const char* what) {
   return FRT_OK;
 }
 
-// One status word per device: bounded waits that run out store FRT_ETIMEOUT.
+// One status word per device: bounded waits that run out store FRT_ETIMEOUT,
+// indices in device memory that are out of range FRT_ERANGE.
 __device__ int g_status_word;
 
 static constexpr int kMaxDevices = 64;
@@ -112,6 +113,8 @@ extern "C" int frt_device_status(int reset, void* stream) {
   }
   if (h == FRT_ETIMEOUT)
     return frt::fail(FRT_ETIMEOUT, "a bounded device wait ran out");
+  if (h == FRT_ERANGE)
+    return frt::fail(FRT_ERANGE, "an index in device memory was out of range");
   return h == 0 ? FRT_OK : frt::fail(FRT_ECUDA, "device status %d", h);
 }
 

@@ -1,0 +1,866 @@
+// paged_attn.cu -- attention over a paged cache held in 4 bits.
+//
+// Per (sequence, kv head) the query rows of all its q heads share the keys:
+// row r of the unit is token r / G, head r % G of the group (G = hq / hkv).
+// A tile of R rows runs over the sequence's keys in chunks, with one pass of
+// the running maximum and sum of the softmax.
+//
+// The codes times their block scales are exact in fp16 (2 + 4 significant
+// bits, 2^-10 .. 2688), so the cache is widened in registers to fp16 and the
+// products run on the tensor cores with fp32 sums; the static scales are
+// applied to the fp32 results.
+#include <cuda_fp16.h>
+
+#include <mutex>
+#include <set>
+#include <utility>
+
+#include "frt_paged.cuh"
+#include "frt_sm100.cuh"
+
+namespace frt {
+namespace {
+
+constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s per wait
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct AttnArgs {
+  int n_seqs, rows, max_q, hq, hkv, group, causal, window;
+  int max_pages;
+  float sm_scale;
+  const uint16_t* q; long ld_q;
+  PagePool pool;
+  const int* page_table;
+  const int* cu_rows;
+  const int* kv_len;
+  const float* k_scale; const float* v_scale;
+  uint16_t* out; long ld_out;
+  float* lse;
+  int* counters;     // [grid], zero between calls
+  float* partials;   // [grid][2] tiles
+  int* status;
+};
+
+// One sequence: its query rows, its keys, and what its work is cut into.
+struct Seq {
+  int r0, Lq, L;        // first row, query rows, keys
+  int chunk0, chunks;   // the chunks any of its queries sees (one at least)
+  int tiles;            // row tiles of each kv head
+  __device__ long work(int hkv) const { return long(chunks) * hkv * tiles; }
+};
+
+template <int R, int CK>
+__device__ __forceinline__ Seq load_seq(const AttnArgs& a, int s, bool report) {
+  Seq q;
+  const long want0 = a.cu_rows ? a.cu_rows[s] : long(s) * a.max_q;
+  const long want1 = a.cu_rows ? a.cu_rows[s + 1] : long(s + 1) * a.max_q;
+  const long r0 = min(max(want0, 0L), long(a.rows));
+  const long r1 = min(min(max(want1, r0), long(a.rows)), r0 + a.max_q);
+  const long cap = long(a.max_pages) * a.pool.page_size;
+  const long want_l = a.kv_len[s];
+  const long L = min(max(want_l, 0L), cap);
+  if (report && (r0 != want0 || r1 != want1 || L != want_l)) atomicExch(a.status, FRT_ERANGE);
+  q.r0 = int(r0);
+  q.Lq = int(r1 - r0);
+  q.L = int(L);
+  q.tiles = (q.Lq * a.group + R - 1) / R;
+  const long first = a.window > 0 ? max(0L, L - q.Lq - a.window + 1) : 0;
+  q.chunk0 = int(first / CK);
+  q.chunks = max(1, int((L + CK - 1) / CK) - q.chunk0);
+  return q;
+}
+
+// A position in the list of all (sequence, row tile, kv head, chunk).
+template <int R, int CK>
+struct Walker {
+  Seq q;
+  int s, unit, chunk;   // unit = tile * hkv + head
+
+  __device__ void start(const AttnArgs& a, int seq, long offset) {
+    s = seq;
+    q = load_seq<R, CK>(a, s, false);
+    unit = int(offset / q.chunks);
+    chunk = int(offset - long(unit) * q.chunks);
+  }
+  // Past the unit's last chunk: to the next unit that has any.
+  __device__ void next_unit(const AttnArgs& a) {
+    chunk = 0;
+    if (++unit < a.hkv * q.tiles) return;
+    unit = 0;
+    do {
+      if (++s >= a.n_seqs) return;
+      q = load_seq<R, CK>(a, s, false);
+    } while (q.tiles == 0);
+  }
+};
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
+      " {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The four bytes of w, two e2m1 codes each, as fp16 pairs.
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(w));
+}
+
+// Two e4m3 codes (low byte first) as an fp16 pair.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t w) {
+  uint32_t h;
+  asm("{\n\t.reg .b16 x;\n\tcvt.u16.u32 x, %1;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, x;\n\t}" : "=r"(h) : "r"(w));
+  return h;
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+template <int BYTES>
+__device__ __forceinline__ void lds(const uint8_t* p, uint32_t (&w)[BYTES / 4]) {
+  if constexpr (BYTES == 4) {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else if constexpr (BYTES == 8) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x; w[1] = v.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < BYTES / 16; ++i) {
+      const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+      w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+    }
+  }
+}
+
+// ------------------------------------------------------------ few rows ----
+//
+// Bound by the cache's bytes (hd * 9/8 per key and kv head), if the widening
+// keeps up: S^T = K Q^T and O^T = V^T P^T on m16n8k16, the keys (and then
+// the head's elements) on the 16 side, so that 8 query rows cost no padding.
+// Any order of the summed index is as good as another as long as both
+// operands agree, so each lane takes whole runs of a key's codes: lane
+// (g = lane / 4, t = lane % 4) widens the quarter t of key g's elements for
+// S, and the eighth g of the elements of keys 2t.. for O.
+//
+// One warp feeds a ring of chunks (bulk copies of page records, or of the
+// four parts of a record where the page is longer than the chunk); each of
+// the W other warps takes 16 keys of every chunk with a softmax state of its
+// own, joined when the unit ends.  The chunks of all units lie on one line
+// that is cut into equal runs, one a CTA: a ragged batch loads every SM
+// alike.  A unit cut by a run's end leaves partial states in the workspace,
+// and the last of its CTAs to finish joins them in order.
+
+template <int HD, int NT>
+struct FewCfg {
+  static constexpr int W = 4;                    // computing warps
+  static constexpr int R = 8 * NT;               // query rows
+  static constexpr int CK = 16 * W;              // keys of a chunk
+  static constexpr int kStage = CK * HD * 9 / 8; // bytes of a chunk
+  static constexpr bool kQRegs = HD / 8 * NT <= 32;
+  static constexpr int kJoin = W * R * HD * 4;   // the warps' sums when a unit ends
+  static constexpr int kQBytes = kQRegs ? 0 : HD / 16 * NT * 32 * 8;
+  static constexpr int kStages = HD == 256 ? 4 : 6;
+  static constexpr int kThreads = 32 * (W + 1);
+  static constexpr int kCtas = HD / 16 * NT <= 8 ? 3 : HD / 16 * NT <= 16 ? 2 : 1;  // per SM
+  static constexpr int kTile = R * (HD + 2);     // floats of one partial state
+  static constexpr int kSmem = kStages * kStage + kJoin + kQBytes + 2 * W * R * 4 + 1024;
+};
+
+template <int HD, int NT>
+__global__ void __launch_bounds__(FewCfg<HD, NT>::kThreads, FewCfg<HD, NT>::kCtas)
+attn_few_kernel(AttnArgs a) {
+  using C = FewCfg<HD, NT>;
+  constexpr int W = C::W, R = C::R, CK = C::CK;
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint8_t* ring = smem;
+  float* join = reinterpret_cast<float*>(ring + C::kStages * C::kStage);
+  uint2* q_smem = reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(join) + C::kJoin);
+  float* join_m = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(q_smem) + C::kQBytes);
+  float* join_l = join_m + W * R;
+  uint64_t* full = reinterpret_cast<uint64_t*>(join_l + W * R);
+  uint64_t* empty = full + C::kStages;
+  uint32_t* valid = reinterpret_cast<uint32_t*>(empty + C::kStages);
+  long* scan = reinterpret_cast<long*>(valid + 8);    // [kThreads / 32] and the start
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(scan + 8);
+  int* last = reinterpret_cast<int*>(scan + 8) + 1;
+
+  const int tid = int(threadIdx.x), warp = tid / 32, lane = tid % 32;
+  pdl_trigger();
+  if (tid == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], W);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  pdl_wait();
+
+  // --- this CTA's run of the line of all chunks ---
+  long total = 0, upto = 0;
+  for (int base = 0; base < a.n_seqs; base += C::kThreads) {
+    const int s = base + tid;
+    long n = 0;
+    if (s < a.n_seqs) n = load_seq<R, CK>(a, s, blockIdx.x == 0).work(a.hkv);
+    long inc = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) scan[warp] = inc;
+    __syncthreads();
+    long before = 0, all = 0;
+    for (int i = 0; i < C::kThreads / 32; ++i) {
+      if (i < warp) before += scan[i];
+      all += scan[i];
+    }
+    upto = total + before + inc;
+    total += all;
+    __syncthreads();
+  }
+  // no more CTAs than chunks
+  const long ctas = total < long(gridDim.x) ? total : long(gridDim.x);
+  const long c = blockIdx.x;
+  if (c >= ctas) return;
+  const long begin = c * total / ctas, end = (c + 1) * total / ctas;
+  if (a.n_seqs > C::kThreads) {  // find the start again, block by block
+    long run = 0;
+    for (int base = 0; base < a.n_seqs; base += C::kThreads) {
+      const int s = base + tid;
+      long n = 0;
+      if (s < a.n_seqs) n = load_seq<R, CK>(a, s, false).work(a.hkv);
+      long inc = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+      }
+      if (lane == 31) scan[warp] = inc;
+      __syncthreads();
+      long before = 0, all = 0;
+      for (int i = 0; i < C::kThreads / 32; ++i) {
+        if (i < warp) before += scan[i];
+        all += scan[i];
+      }
+      __syncthreads();
+      const long hi = run + before + inc;
+      if (n > 0 && begin >= hi - n && begin < hi) {
+        scan[6] = s;
+        scan[7] = begin - (hi - n);
+      }
+      run += all;
+    }
+  } else if (tid < a.n_seqs) {
+    const long n = load_seq<R, CK>(a, tid, false).work(a.hkv);
+    if (n > 0 && begin >= upto - n && begin < upto) {
+      scan[6] = tid;
+      scan[7] = begin - (upto - n);
+    }
+  }
+  __syncthreads();
+  Walker<R, CK> w;
+  w.start(a, int(scan[6]), scan[7]);
+
+  const int ps = a.pool.page_size;
+  const int sub = ps < CK ? ps : CK;  // keys of one record's piece in a chunk
+
+  if (warp == W) {
+    // ------------------------------------------------------------ the feed --
+    int stage = 0;
+    uint32_t phase = 0;
+    const int n_sub = CK / sub;
+    const bool parts = ps > CK;
+    long issued = 0;
+    for (long x = begin; x < end; ++x) {
+      const int head = w.unit % a.hkv;
+      const int key0 = (w.q.chunk0 + w.chunk) * CK;
+      // lane i: piece i of the chunk
+      const int piece_key = parts ? key0 : key0 + lane * sub;
+      int page = -1;
+      if (lane < (parts ? 4 : n_sub) && piece_key < w.q.L) {
+        page = a.page_table[long(w.s) * a.max_pages + (piece_key >> a.pool.shift)];
+        if (page < 0 || page >= a.pool.n_pages) {
+          atomicExch(a.status, FRT_ERANGE);
+          page = -1;
+        }
+      }
+      const uint32_t have = __ballot_sync(0xffffffffu, page >= 0);
+      bool ok = true;
+      if (lane == 0) {
+        ok = mbar_wait_bounded(&empty[stage], phase ^ 1u, kWaitNs, abort_flag);
+        if (!ok) {
+          atomicExch(a.status, FRT_ETIMEOUT);
+          *abort_flag = 1;
+        } else {
+          valid[stage] = have;
+          const uint32_t bytes = parts ? (have ? C::kStage : 0u)
+                                       : __popc(have) * (sub * HD * 9 / 8);
+          mbar_arrive_expect_tx(&full[stage], bytes);
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      __syncwarp();
+      if (page >= 0) {
+        const uint8_t* rec = a.pool.base + (long(page) * a.pool.hkv + head) * a.pool.record_bytes;
+        uint8_t* dst = ring + stage * C::kStage;
+        if (!parts) {
+          bulk_load(dst + lane * (sub * HD * 9 / 8), rec, sub * HD * 9 / 8, &full[stage]);
+        } else {  // lane 0 .. 3: key codes, key scales, value codes, value scales
+          const int at = key0 & (ps - 1);
+          rec += (lane & 2 ? a.pool.record_bytes / 2 : 0) +
+                 (lane & 1 ? ps * (HD / 2) + at * (HD / 16) : at * (HD / 2));
+          dst += (lane & 2 ? C::kStage / 2 : 0) + (lane & 1 ? CK * (HD / 2) : 0);
+          bulk_load(dst, rec, lane & 1 ? CK * (HD / 16) : CK * (HD / 2), &full[stage]);
+        }
+      }
+      ++issued;
+      if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
+      if (++w.chunk == w.q.chunks && x + 1 < end) w.next_unit(a);
+    }
+    // after a wait that ran out: no exit with copies in flight
+    if (*abort_flag && lane == 0) {
+      for (long i = issued - C::kStages < 0 ? 0 : issued - C::kStages; i < issued; ++i)
+        mbar_wait_bounded(&full[i % C::kStages], uint32_t(i / C::kStages) & 1u, kWaitNs, nullptr);
+    }
+    return;
+  }
+
+  // ------------------------------------------------------- the arithmetic --
+  const int g = lane / 4, t = lane % 4;
+  // keys of this lane in a group of 16 (the second eight: + 8): its row of
+  // S^T, and the two rows of the summed index of O^T.  The order is the one
+  // that spreads both reads over the banks.
+  const int key_s = (g & ~1) + ((g ^ (g >> 1)) & 1);
+  const int key_o[2] = {2 * t + (t & 1), 2 * t + ((t & 1) ^ 1)};
+  const float kscale = *a.k_scale * a.sm_scale * kLog2e;
+  const float vscale = *a.v_scale;
+  int stage = 0;
+  uint32_t phase = 0;
+
+  for (long x = begin; x < end;) {
+    const long seg0 = x;
+    const int n_here = int(min(long(w.q.chunks - w.chunk), end - x));
+    const bool from_start = w.chunk == 0, to_end = w.chunk + n_here == w.q.chunks;
+    const int head = w.unit % a.hkv, tile = w.unit / a.hkv;
+    const int rows_here = w.q.Lq * a.group;
+
+    // Q fragments: row g (+ 8 per nt), elements t * HD/4 .., scaled by a
+    // power of two that brings the row's largest below 2
+    uint32_t qf[C::kQRegs ? NT : 1][C::kQRegs ? HD / 8 : 1];
+    float cq[NT][2], m[NT][2], l[NT][2];
+    int lim_hi[NT][2], lim_lo[NT][2];
+    int tile_hi = 0, tile_lo = 0x7fffffff, all_hi = 0x7fffffff, all_lo = 0;
+    if constexpr (!C::kQRegs) named_bar_sync(1, W * 32);  // the last unit's reads of q_smem
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      if (!C::kQRegs && nt % W != warp % W && NT >= W) continue;
+      const int r = tile * R + nt * 8 + g;
+      uint32_t raw[HD / 8];
+      float big = 0.0f;
+      if (r < rows_here) {
+        const int token = r / a.group;
+        const uint16_t* src = a.q + long(w.q.r0 + token) * a.ld_q +
+                              long(head * a.group + r - token * a.group) * HD + t * (HD / 4);
+#pragma unroll
+        for (int i = 0; i < HD / 32; ++i) {
+          const uint4 v = reinterpret_cast<const uint4*>(src)[i];
+          raw[4 * i] = v.x; raw[4 * i + 1] = v.y; raw[4 * i + 2] = v.z; raw[4 * i + 3] = v.w;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < HD / 8; ++i) raw[i] = 0;
+      }
+#pragma unroll
+      for (int i = 0; i < HD / 8; ++i)
+        big = fmaxf(big, fmaxf(fabsf(__uint_as_float(raw[i] << 16)),
+                               fabsf(__uint_as_float(raw[i] & 0xFFFF0000u))));
+      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+      int e = int(__float_as_uint(big) >> 23);  // 2^(e - 127) <= big
+      if (e < 1 || e > 253) e = 127;            // zero, subnormal, infinite: as it is
+      const float down = __uint_as_float(uint32_t(254 - e) << 23);
+      const float up = __uint_as_float(uint32_t(e) << 23);
+#pragma unroll
+      for (int i = 0; i < HD / 8; ++i) {
+        raw[i] = pack_f16x2(__uint_as_float(raw[i] << 16) * down,
+                            __uint_as_float(raw[i] & 0xFFFF0000u) * down);
+        if constexpr (C::kQRegs) qf[nt][i] = raw[i];
+      }
+      if constexpr (!C::kQRegs) {
+#pragma unroll
+        for (int j = 0; j < HD / 16; ++j)
+          q_smem[(nt * (HD / 16) + j) * 32 + lane] = make_uint2(raw[2 * j], raw[2 * j + 1]);
+        if (t == 0) join_m[nt * 8 + g] = up;
+      } else {
+#pragma unroll
+        for (int e2 = 0; e2 < 2; ++e2)
+          cq[nt][e2] = __shfl_sync(0xffffffffu, up, (2 * t + e2) * 4) * kscale;
+      }
+    }
+    if constexpr (!C::kQRegs) {
+      named_bar_sync(1, W * 32);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e2 = 0; e2 < 2; ++e2) cq[nt][e2] = join_m[nt * 8 + 2 * t + e2] * kscale;
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e2 = 0; e2 < 2; ++e2) {
+        const int r = tile * R + nt * 8 + 2 * t + e2;
+        int hi = 0, lo = 0;
+        if (r < rows_here) {
+          const int place = w.q.L - w.q.Lq + r / a.group;
+          hi = a.causal ? min(w.q.L, place + 1) : w.q.L;
+          lo = a.window > 0 ? max(0, place - a.window + 1) : 0;
+          tile_hi = max(tile_hi, hi);
+          tile_lo = min(tile_lo, lo);
+          all_hi = min(all_hi, hi);
+          all_lo = max(all_lo, lo);
+        }
+        lim_hi[nt][e2] = hi;
+        lim_lo[nt][e2] = lo;
+        m[nt][e2] = -INFINITY;
+        l[nt][e2] = 0.0f;
+      }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {  // over t: the tile's limits
+      tile_hi = max(tile_hi, __shfl_xor_sync(0xffffffffu, tile_hi, o));
+      tile_lo = min(tile_lo, __shfl_xor_sync(0xffffffffu, tile_lo, o));
+      all_hi = min(all_hi, __shfl_xor_sync(0xffffffffu, all_hi, o));
+      all_lo = max(all_lo, __shfl_xor_sync(0xffffffffu, all_lo, o));
+    }
+    float o_acc[NT][HD / 16][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < HD / 16; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o_acc[nt][i][j] = 0.0f;
+
+    for (int n = 0; n < n_here; ++n, ++x) {
+      const int key0 = (w.q.chunk0 + w.chunk + n) * CK + warp * 16;
+      // every lane waits: each reads what the copies wrote
+      const bool got = mbar_wait_bounded(&full[stage], phase, kWaitNs, abort_flag);
+      if (!got && lane == 0) {
+        atomicExch(a.status, FRT_ETIMEOUT);
+        *abort_flag = 1;
+      }
+      const int piece = ps < CK ? warp * 16 / sub : 0;
+      if (__all_sync(0xffffffffu, got) && key0 < tile_hi && key0 + 16 > tile_lo &&
+          (valid[stage] >> piece & 1)) {
+        const uint8_t* kc = ring + stage * C::kStage + piece * (sub * HD * 9 / 8);
+        const int at = warp * 16 - piece * sub;
+        const uint8_t* ks = kc + sub * (HD / 2) + at * (HD / 16);
+        const uint8_t* vc = kc + sub * (HD / 2 + HD / 16) + at * (HD / 2);
+        const uint8_t* vs = kc + sub * (HD + HD / 16) + at * (HD / 16);
+        kc += at * (HD / 2);
+        const bool masked = key0 + 16 > all_hi || key0 < all_lo;
+
+        // S^T, 16 keys x 8 NT rows
+        uint32_t kw[2][HD / 32];
+        uint32_t kscl[2][(HD + 127) / 128];  // pairs of block scales, fp16
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          lds<HD / 8>(kc + (key_s + 8 * f) * (HD / 2) + t * (HD / 8), kw[f]);
+          const uint8_t* sp = ks + (key_s + 8 * f) * (HD / 16) + t * (HD / 64);
+          if constexpr (HD == 64) {
+            kscl[f][0] = e4m3x2_to_f16(*sp);
+          } else if constexpr (HD == 128) {
+            kscl[f][0] = e4m3x2_to_f16(*reinterpret_cast<const uint16_t*>(sp));
+          } else {
+            const uint32_t v = *reinterpret_cast<const uint32_t*>(sp);
+            kscl[f][0] = e4m3x2_to_f16(v & 0xFFFFu);
+            kscl[f][1] = e4m3x2_to_f16(v >> 16);
+          }
+        }
+        float s[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[nt][i] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < HD / 32; ++i) {  // 8 codes of each key: half a block
+          uint32_t h[2][4];
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+            e2m1x8_to_f16(kw[f][i], h[f]);
+            const uint32_t pair = kscl[f][i / 4];
+            const uint32_t sc = __byte_perm(pair, 0, i / 2 % 2 ? 0x3232 : 0x1010);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) h[f][k] = hmul2(h[f][k], sc);
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              uint32_t b0, b1;
+              if constexpr (C::kQRegs) {
+                b0 = qf[nt][4 * i + 2 * k];
+                b1 = qf[nt][4 * i + 2 * k + 1];
+              } else {
+                const uint2 b = q_smem[(nt * (HD / 16) + 2 * i + k) * 32 + lane];
+                b0 = b.x; b1 = b.y;
+              }
+              mma_f16(s[nt], h[0][2 * k], h[1][2 * k], h[0][2 * k + 1], h[1][2 * k + 1], b0, b1);
+            }
+        }
+
+        // softmax: base-2 scores against a running maximum that is raised
+        // only when a score passes it by more than 2^8 (the weights then
+        // stay within fp16), so most groups pass without the reduction
+        bool grow = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float v = s[nt][i] * cq[nt][i & 1];
+            if (masked) {
+              const int key = key0 + key_s + 8 * (i >> 1);
+              if (key >= lim_hi[nt][i & 1] || key < lim_lo[nt][i & 1]) v = -INFINITY;
+            }
+            s[nt][i] = v;
+            grow |= v > m[nt][i & 1] + 8.0f;
+          }
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e2 = 0; e2 < 2; ++e2) {
+              float v = fmaxf(s[nt][e2], s[nt][e2 + 2]);
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+              v = fmaxf(v, m[nt][e2]);
+              const float f = v == -INFINITY ? 1.0f : ex2(m[nt][e2] - v);
+              m[nt][e2] = v;
+              l[nt][e2] *= f;
+#pragma unroll
+              for (int i = 0; i < HD / 16; ++i) {
+                o_acc[nt][i][e2] *= f;
+                o_acc[nt][i][e2 + 2] *= f;
+              }
+            }
+        }
+        uint32_t p[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float mm = m[nt][i & 1];
+            s[nt][i] = ex2(s[nt][i] - (mm == -INFINITY ? 0.0f : mm));
+            l[nt][i & 1] += s[nt][i];
+          }
+          p[nt][0] = movmatrix_trans(pack_f16x2(s[nt][0], s[nt][1]));
+          p[nt][1] = movmatrix_trans(pack_f16x2(s[nt][2], s[nt][3]));
+        }
+
+        // O^T += V^T P^T
+        uint32_t vw[2][2][HD / 64];       // [eight][key][words]
+        uint32_t vscl[2][HD == 256 ? 2 : 1];  // (key 0, key 1) scales, fp16
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          uint32_t sb[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int key = key_o[k] + 8 * f;
+            lds<HD / 16>(vc + key * (HD / 2) + g * (HD / 16), vw[f][k]);
+            const uint8_t* sp = vs + key * (HD / 16);
+            if constexpr (HD == 64) sb[k] = sp[g / 2];
+            else if constexpr (HD == 128) sb[k] = sp[g];
+            else sb[k] = *reinterpret_cast<const uint16_t*>(sp + 2 * g);
+            // behind the sequence's end the page may hold anything
+            if (masked && key0 + key >= w.q.L) sb[k] = 0;
+          }
+          vscl[f][0] = e4m3x2_to_f16(__byte_perm(sb[0], sb[1], 0x0040));
+          if constexpr (HD == 256) vscl[f][1] = e4m3x2_to_f16(__byte_perm(sb[0], sb[1], 0x0051));
+        }
+#pragma unroll
+        for (int i = 0; i < HD / 64; ++i) {  // 8 elements of every key
+          uint32_t even[2][4], odd[2][4];
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+            const uint32_t w0 = vw[f][0][i], w1 = vw[f][1][i];
+            constexpr uint32_t kLow = 0x0F0F0F0Fu;
+            e2m1x8_to_f16((w0 & kLow) | ((w1 << 4) & ~kLow), even[f]);
+            e2m1x8_to_f16(((w0 >> 4) & kLow) | (w1 & ~kLow), odd[f]);
+            const uint32_t sc = vscl[f][HD == 256 ? i / 2 : 0];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              even[f][k] = hmul2(even[f][k], sc);
+              odd[f][k] = hmul2(odd[f][k], sc);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_f16(o_acc[nt][4 * i + k], even[0][k], odd[0][k], even[1][k], odd[1][k],
+                      p[nt][0], p[nt][1]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[stage]);
+      if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
+    }
+
+    // --- the unit (or this CTA's share of it) ends: join the warps ---
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e2 = 0; e2 < 2; ++e2)
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) l[nt][e2] += __shfl_xor_sync(0xffffffffu, l[nt][e2], o);
+    named_bar_sync(1, W * 32);  // join_m / join (and its use before) are free
+    if (g == 0) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e2 = 0; e2 < 2; ++e2) {
+          join_m[warp * R + nt * 8 + 2 * t + e2] = m[nt][e2];
+          join_l[warp * R + nt * 8 + 2 * t + e2] = l[nt][e2];
+        }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < HD / 16; ++i)
+#pragma unroll
+        for (int e2 = 0; e2 < 2; ++e2)
+          *reinterpret_cast<float2*>(join + (warp * R + nt * 8 + 2 * t + e2) * HD + g * (HD / 8) + 2 * i) =
+              make_float2(o_acc[nt][i][e2], o_acc[nt][i][e2 + 2]);
+    named_bar_sync(1, W * 32);
+
+    const bool whole = from_start && to_end;
+    float* part = a.partials + (2 * c + (from_start ? 1 : 0)) * C::kTile;
+    // parts of a cut unit: CTAs first .. final
+    const long unit0 = seg0 - w.chunk;
+    const long first = ((unit0 + 1) * ctas - 1) / total;
+    const long final = ((unit0 + w.q.chunks) * ctas - 1) / total;
+    for (int i = tid; i < R * (HD / 4); i += W * 32) {
+      const int r = i / (HD / 4), d = i % (HD / 4) * 4;
+      float mm = -INFINITY, ll = 0.0f;
+#pragma unroll
+      for (int k = 0; k < W; ++k) mm = fmaxf(mm, join_m[k * R + r]);
+      float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int k = 0; k < W; ++k) {
+        const float f = mm == -INFINITY ? 0.0f : ex2(join_m[k * R + r] - mm);
+        const float4 v = *reinterpret_cast<const float4*>(join + (k * R + r) * HD + d);
+        ll += join_l[k * R + r] * f;
+        acc.x += v.x * f; acc.y += v.y * f; acc.z += v.z * f; acc.w += v.w * f;
+      }
+      if (!whole) {
+        *reinterpret_cast<float4*>(part + r * HD + d) = acc;
+        if (d == 0) {
+          part[R * HD + r] = mm;
+          part[R * HD + R + r] = ll;
+        }
+        continue;
+      }
+      const int row = tile * R + r;
+      if (row >= rows_here) continue;
+      const int token = row / a.group, h = head * a.group + row - token * a.group;
+      const float inv = ll > 0.0f ? vscale / ll : ll * vscale;  // no keys: 0; NaN stays
+      *reinterpret_cast<uint2*>(a.out + long(w.q.r0 + token) * a.ld_out + long(h) * HD + d) =
+          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+      if (d == 0 && a.lse)
+        a.lse[long(w.q.r0 + token) * a.hq + h] = mm == -INFINITY ? mm : (mm + log2f(ll)) * kLn2;
+    }
+    if (!whole) {
+      __threadfence();
+      named_bar_sync(1, W * 32);
+      if (tid == 0) {
+        const int before = atomicAdd(&a.counters[first], 1);
+        *last = before == int(final - first);
+        if (*last) a.counters[first] = 0;
+      }
+      named_bar_sync(1, W * 32);
+      if (*last) {
+        __threadfence();
+        for (int i = tid; i < R * (HD / 4); i += W * 32) {
+          const int r = i / (HD / 4), d = i % (HD / 4) * 4;
+          const int row = tile * R + r;
+          if (row >= rows_here) continue;
+          float mm = -INFINITY, ll = 0.0f;
+          for (long k = first; k <= final; ++k)
+            mm = fmaxf(mm, __ldcg(a.partials + (2 * k + (k == first)) * C::kTile + R * HD + r));
+          float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+          for (long k = first; k <= final; ++k) {
+            const float* pt = a.partials + (2 * k + (k == first)) * C::kTile;
+            const float f = mm == -INFINITY ? 0.0f : ex2(__ldcg(pt + R * HD + r) - mm);
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(pt + r * HD + d));
+            ll += __ldcg(pt + R * HD + R + r) * f;
+            acc.x += v.x * f; acc.y += v.y * f; acc.z += v.z * f; acc.w += v.w * f;
+          }
+          const int token = row / a.group, h = head * a.group + row - token * a.group;
+          const float inv = ll > 0.0f ? vscale / ll : ll * vscale;
+          *reinterpret_cast<uint2*>(a.out + long(w.q.r0 + token) * a.ld_out + long(h) * HD + d) =
+              make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv),
+                         pack_bf16x2(acc.z * inv, acc.w * inv));
+          if (d == 0 && a.lse)
+            a.lse[long(w.q.r0 + token) * a.hq + h] = mm == -INFINITY ? mm : (mm + log2f(ll)) * kLn2;
+        }
+      }
+    }
+    w.chunk += n_here;
+    if (w.chunk == w.q.chunks && x < end) w.next_unit(a);
+  }
+}
+
+// ---------------------------------------------------------------- launch --
+
+// Opt a kernel into its shared memory on the current device, before any
+// thread's first launch of it there.
+int allow_smem(const void* kern, int bytes) {
+  static std::mutex mu;
+  static std::set<std::pair<int, const void*>> done;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  std::lock_guard<std::mutex> lock(mu);
+  if (done.count({dev, kern})) return FRT_OK;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+    cudaGetLastError();
+    return fail(FRT_ECUDA, "frt_paged_attention_fp4: %d bytes of shared memory refused", bytes);
+  }
+  done.insert({dev, kern});
+  return FRT_OK;
+}
+
+template <int HD, int NT>
+struct Few {
+  using C = FewCfg<HD, NT>;
+  static int grid() { return num_sms() * C::kCtas; }
+  static size_t workspace() {
+    return (size_t(grid()) * 4 + 255) / 256 * 256 + size_t(grid()) * 2 * C::kTile * 4;
+  }
+  static int launch(AttnArgs a, void* ws, long most_chunks, cudaStream_t s) {
+    auto kern = attn_few_kernel<HD, NT>;
+    if (int rc = allow_smem(reinterpret_cast<const void*>(kern), C::kSmem)) return rc;
+    a.counters = static_cast<int*>(ws);
+    a.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) +
+                                          (size_t(grid()) * 4 + 255) / 256 * 256);
+    const int n = most_chunks < grid() ? int(most_chunks) : grid();
+    return launch_pdl("frt_paged_attention_fp4", kern, dim3(n), dim3(C::kThreads), C::kSmem, s, a);
+  }
+};
+
+// f(Few<HD, NT>) for the head size and the rows of one kv head.
+template <typename F>
+auto with_variant(int hd, long rows_per_head, F f) {
+  if (hd == 64)
+    return rows_per_head <= 8 ? f(Few<64, 1>{}) : rows_per_head <= 16 ? f(Few<64, 2>{}) : f(Few<64, 4>{});
+  if (hd == 128)
+    return rows_per_head <= 8 ? f(Few<128, 1>{}) : rows_per_head <= 16 ? f(Few<128, 2>{}) : f(Few<128, 4>{});
+  return rows_per_head <= 8 ? f(Few<256, 1>{}) : f(Few<256, 2>{});
+}
+
+bool head_counts_ok(int n_seqs, int max_q, int hq, int hkv, int hd) {
+  return n_seqs >= 0 && max_q >= 0 && hkv >= 1 && hkv <= 65536 && hq >= hkv && hq <= 65536 &&
+         hq % hkv == 0 && (hd == 64 || hd == 128 || hd == 256) &&
+         long(max_q) * (hq / hkv) <= 0x40000000L;
+}
+
+}  // namespace
+}  // namespace frt
+
+extern "C" size_t frt_paged_attention_workspace_size(int n_seqs, int max_q, int hq, int hkv, int hd) {
+  if (!frt::head_counts_ok(n_seqs, max_q, hq, hkv, hd)) return 0;
+  return frt::with_variant(hd, long(max_q) * (hq / hkv), [](auto v) { return v.workspace(); });
+}
+
+extern "C" int frt_paged_attention_fp4(const frt_paged_attn_desc* d, void* stream) {
+  using frt::aligned;
+  frt::clear_error();
+  FRT_REQUIRE(d, FRT_EINVAL, "descriptor is NULL");
+  FRT_REQUIRE(d->hd == 64 || d->hd == 128 || d->hd == 256, FRT_ESHAPE,
+              "hd must be 64, 128 or 256, got %d", d->hd);
+  FRT_REQUIRE(d->rows >= 0 && frt::head_counts_ok(d->n_seqs, d->max_q, d->hq, d->hkv, d->hd),
+              FRT_ESHAPE, "bad n_seqs / rows / max_q / heads: %d, %d, %d, %d, %d", d->n_seqs,
+              d->rows, d->max_q, d->hq, d->hkv);
+  const size_t rec = frt_kv_record_bytes(FRT_PAGE_E2M1, d->page_size, d->hd);
+  FRT_REQUIRE(rec > 0, FRT_ESHAPE, "page_size must be a power of two in [16, 1024], got %d",
+              d->page_size);
+  FRT_REQUIRE(d->max_pages >= 0 && d->n_pages >= 0 &&
+                  long(d->max_pages) * d->page_size <= 0x40000000L,
+              FRT_ESHAPE, "bad max_pages / n_pages: %d, %d", d->max_pages, d->n_pages);
+  FRT_REQUIRE(d->window >= 0 && (d->window == 0 || d->causal), FRT_EINVAL,
+              "a window must be >= 0 and needs causal");
+  if (d->n_seqs == 0 || d->rows == 0 || d->max_q == 0) return FRT_OK;
+  FRT_REQUIRE(d->q && d->out && d->kv_len && d->k_scale && d->v_scale, FRT_EINVAL,
+              "q, out, kv_len, k_scale and v_scale are required");
+  FRT_REQUIRE(d->max_pages == 0 || (d->pool && d->page_table), FRT_EINVAL,
+              "pool and page_table are required");
+  FRT_REQUIRE(aligned(d->q, 16) && aligned(d->out, 16) && aligned(d->pool, 16) &&
+                  d->ld_q % 8 == 0 && d->ld_out % 8 == 0,
+              FRT_EALIGN, "q, out and pool must be 16-byte aligned with row strides that are "
+              "multiples of 8");
+  FRT_REQUIRE(d->ld_q >= long(d->hq) * d->hd && d->ld_out >= long(d->hq) * d->hd, FRT_ESHAPE,
+              "a row stride is less than hq * hd");
+  FRT_REQUIRE(aligned(d->page_table, 4) && aligned(d->cu_rows, 4) && aligned(d->kv_len, 4) &&
+                  aligned(d->lse, 4) && aligned(d->k_scale, 4) && aligned(d->v_scale, 4),
+              FRT_EALIGN, "page_table, cu_rows, kv_len, lse and the scales must be 4-byte aligned");
+  const size_t need =
+      frt_paged_attention_workspace_size(d->n_seqs, d->max_q, d->hq, d->hkv, d->hd);
+  FRT_REQUIRE(d->workspace, FRT_EINVAL, "workspace is required");
+  FRT_REQUIRE(aligned(d->workspace, 16), FRT_EALIGN, "workspace must be 16-byte aligned");
+  FRT_REQUIRE(d->workspace_bytes >= need, FRT_ERANGE, "workspace has %zu bytes, %zu needed",
+              d->workspace_bytes, need);
+  frt::AttnArgs a{};
+  a.n_seqs = d->n_seqs; a.rows = d->rows; a.max_q = d->max_q; a.hq = d->hq; a.hkv = d->hkv;
+  a.group = d->hq / d->hkv; a.causal = d->causal != 0; a.window = d->window;
+  a.max_pages = d->max_pages; a.sm_scale = d->sm_scale;
+  a.q = d->q; a.ld_q = d->ld_q;
+  a.pool = frt::make_page_pool(const_cast<void*>(d->pool), FRT_PAGE_E2M1, d->page_size, d->n_pages,
+                               d->hkv, d->hd);
+  a.page_table = d->page_table; a.cu_rows = d->cu_rows; a.kv_len = d->kv_len;
+  a.k_scale = d->k_scale; a.v_scale = d->v_scale;
+  a.out = d->out; a.ld_out = d->ld_out; a.lse = d->lse;
+  a.status = frt::device_status_ptr();
+  FRT_REQUIRE(a.status, FRT_ECUDA, "device status word unavailable");
+  const long per_head = long(d->max_q) * a.group;
+  return frt::with_variant(d->hd, per_head, [&](auto v) {
+    using C = typename decltype(v)::C;
+    const long tiles = (per_head + C::R - 1) / C::R;
+    const long chunks = (long(d->max_pages) * d->page_size + C::CK - 1) / C::CK;
+    const long most = long(d->n_seqs) * d->hkv * tiles;
+    // no sequence has fewer than one chunk
+    const long all = most >= 0x7fffffffL ? most : most * (chunks > 1 ? chunks : 1);
+    return v.launch(a, d->workspace, all, static_cast<cudaStream_t>(stream));
+  });
+}

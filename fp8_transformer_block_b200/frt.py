@@ -27,6 +27,9 @@ FRT_PACK_CONCAT, FRT_PACK_QK_INTERLEAVE, FRT_PACK_GATE_UP_BLOCKS = 0, 1, 2
 FRT_EPI_BF16, FRT_EPI_GEGLU_E4M3, FRT_EPI_GELU_E4M3 = 0, 1, 2
 FRT_CHAIN_FUSED_ROPE, FRT_CHAIN_UNFUSED = 0, 1
 FRT_PEAK_OPERANDS_GAUSSIAN, FRT_PEAK_OPERANDS_LOW_TOGGLE = 0, 1
+FRT_ROPE_SCALE_NONE, FRT_ROPE_SCALE_LINEAR, FRT_ROPE_SCALE_BASE, FRT_ROPE_SCALE_PARTS = 0, 1, 2, 3
+FRT_ROPE_PAIRS, FRT_ROPE_HALF = 0, 1
+FRT_PAGE_BF16, FRT_PAGE_E2M1 = 0, 1
 
 STATUS_NAMES = {0: "FRT_OK", -1: "FRT_EINVAL", -2: "FRT_ESHAPE",
                 -3: "FRT_EALIGN", -4: "FRT_ERANGE", -5: "FRT_ECUDA",
@@ -85,6 +88,29 @@ class frt_ffn_desc(C.Structure):
     ]
 
 
+class frt_qk_rope_desc(C.Structure):
+    """Mirror of ``frt_qk_rope_desc`` in include/frt.h (same field order)."""
+    _fields_ = [
+        ("rows", _i), ("hq", _i), ("hkv", _i), ("hd", _i), ("rot", _i), ("layout", _i),
+        ("eps", _f), ("qkv", _p), ("ld_qkv", _l), ("q_norm", _p), ("k_norm", _p),
+        ("rope", _p), ("n_pos", _i), ("positions", _p),
+        ("q_out", _p), ("ld_q", _l), ("k_out", _p), ("ld_k", _l), ("v_out", _p), ("ld_v", _l),
+        ("format", _i), ("page_size", _i), ("n_pages", _i), ("pool", _p), ("slots", _p),
+        ("k_scale", _p), ("v_scale", _p),
+    ]
+
+
+class frt_paged_attn_desc(C.Structure):
+    """Mirror of ``frt_paged_attn_desc`` in include/frt.h (same field order)."""
+    _fields_ = [
+        ("n_seqs", _i), ("rows", _i), ("max_q", _i), ("hq", _i), ("hkv", _i), ("hd", _i),
+        ("page_size", _i), ("max_pages", _i), ("n_pages", _i), ("causal", _i), ("window", _i),
+        ("sm_scale", _f), ("q", _p), ("ld_q", _l), ("pool", _p), ("page_table", _p),
+        ("cu_rows", _p), ("kv_len", _p), ("k_scale", _p), ("v_scale", _p),
+        ("out", _p), ("ld_out", _l), ("lse", _p), ("workspace", _p), ("workspace_bytes", _z),
+    ]
+
+
 _SIGS = {
     "frt_last_error": (C.c_char_p, []),
     "frt_version": (_i, []),
@@ -117,6 +143,13 @@ _SIGS = {
     "frt_gelu_quant_fp8": (_i, [_i, _i, _p, _l, _p, _p, _p, _p]),
     "frt_ada_rms_tail": (_i, [_i, _i, _f, _p, _p, _p, _l, _p, _l, _p, _p]),
     "frt_style_project": (_i, [_i, _i, _i, _p, _l, _p, _l, _p, _p, _l, _p, _l, _i, _p]),
+    "frt_build_rope_table_scaled": (_i, [_i, _i, _l, _d, _i, _d, _d, _d, _d, _d, _p, _p]),
+    "frt_kv_record_bytes": (_z, [_i, _i, _i]),
+    "frt_qk_norm_rope": (_i, [C.POINTER(frt_qk_rope_desc), _p]),
+    "frt_paged_kv_append": (_i, [C.POINTER(frt_qk_rope_desc), _p]),
+    "frt_paged_kv_read": (_i, [C.POINTER(frt_qk_rope_desc), _p]),
+    "frt_paged_attention_workspace_size": (_z, [_i, _i, _i, _i, _i]),
+    "frt_paged_attention_fp4": (_i, [C.POINTER(frt_paged_attn_desc), _p]),
     "frt_gemm_plan_info": (_i, [_i, _i, _i, _i, _p, _i]),
     "frt_peak_fp8_mma": (_i, [_i, _i, _i, _p]),
     "frt_peak_copy": (_i, [_p, _p, C.c_size_t, _p]),
@@ -309,6 +342,41 @@ def frt_style_project(rows, K, N, cond, ld_cond, w, ldw, bias, style_out, ld_sty
                                   ptr(style_out), ld_style, ptr(fin_out), ld_fin, fin_col0,
                                   _stream(stream)),
            "frt_style_project")
+
+
+def frt_build_rope_table_scaled(M, rot, P, theta, scaling, factor, orig_len, low_turns,
+                                high_turns, amplitude, rope_out, stream=None):
+    """fp32 rotary table [M, rot] with scaled frequencies."""
+    return _check(_lib.frt_build_rope_table_scaled(
+        M, rot, P, theta, scaling, factor, orig_len, low_turns, high_turns, amplitude,
+        ptr(rope_out), _stream(stream)), "frt_build_rope_table_scaled")
+
+
+def frt_kv_record_bytes(format, page_size, hd) -> int:
+    """Bytes of one kv head's record in a page (0: not a supported page)."""
+    return int(_lib.frt_kv_record_bytes(format, page_size, hd))
+
+
+def frt_qk_norm_rope(desc: frt_qk_rope_desc, stream=None):
+    return _check(_lib.frt_qk_norm_rope(C.byref(desc), _stream(stream)), "frt_qk_norm_rope")
+
+
+def frt_paged_kv_append(desc: frt_qk_rope_desc, stream=None):
+    return _check(_lib.frt_paged_kv_append(C.byref(desc), _stream(stream)),
+                  "frt_paged_kv_append")
+
+
+def frt_paged_kv_read(desc: frt_qk_rope_desc, stream=None):
+    return _check(_lib.frt_paged_kv_read(C.byref(desc), _stream(stream)), "frt_paged_kv_read")
+
+
+def frt_paged_attention_workspace_size(n_seqs, max_q, hq, hkv, hd) -> int:
+    return int(_lib.frt_paged_attention_workspace_size(n_seqs, max_q, hq, hkv, hd))
+
+
+def frt_paged_attention_fp4(desc: frt_paged_attn_desc, stream=None):
+    return _check(_lib.frt_paged_attention_fp4(C.byref(desc), _stream(stream)),
+                  "frt_paged_attention_fp4")
 
 
 FRT_PLAN_INFO_LEN = 10

@@ -113,3 +113,32 @@ def ffn_desc(**kw) -> frt.frt_ffn_desc:
     for k, v in kw.items():
         setattr(d, k, frt.ptr(v) if k in ptr_fields else v)
     return d
+
+
+# ---------------------------------------------------------- paged cache ----
+
+def qk_rope_desc(**kw) -> frt.frt_qk_rope_desc:
+    """Build an frt_qk_rope_desc; tensor fields accept tensors/ints/None."""
+    return _fill(frt.frt_qk_rope_desc(), kw)
+
+
+def paged_attn_desc(**kw) -> frt.frt_paged_attn_desc:
+    """Build an frt_paged_attn_desc; tensor fields accept tensors/ints/None."""
+    return _fill(frt.frt_paged_attn_desc(), kw)
+
+
+def _fill(d, kw):
+    ptr_fields = {name for name, typ in d._fields_ if typ is frt._p}
+    for k, v in kw.items():
+        setattr(d, k, frt.ptr(v) if k in ptr_fields else v)
+    return d
+
+
+def kv_pool(n_pages: int, hkv: int, page_size: int, hd: int, format=frt.FRT_PAGE_E2M1,
+            device="cuda") -> torch.Tensor:
+    """Zero-filled page pool [n_pages, hkv, record] (zero pages hold zeros in
+    both formats)."""
+    rec = frt.frt_kv_record_bytes(format, page_size, hd)
+    if rec == 0:
+        raise ValueError(f"no page format {format} with page_size {page_size}, hd {hd}")
+    return torch.zeros(n_pages, hkv, rec, dtype=torch.uint8, device=device)

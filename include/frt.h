@@ -48,7 +48,9 @@ enum {
   FRT_EINVAL = -1,   /* null pointer, bad enum, bad scalar                 */
   FRT_ESHAPE = -2,   /* dimension outside what the kernel supports         */
   FRT_EALIGN = -3,   /* pointer or stride not aligned as required          */
-  FRT_ERANGE = -4,   /* P + M > T, workspace too small, row capacity       */
+  FRT_ERANGE = -4,   /* P + M > T, workspace too small, row capacity; from
+                        frt_device_status: an index in device memory was
+                        out of range and was not followed                  */
   FRT_ECUDA = -5,    /* CUDA reported an error at launch                   */
   FRT_ETIMEOUT = -6  /* a bounded device-side wait ran out                 */
 };
@@ -61,7 +63,9 @@ int frt_version(void);
 
 /* Read (and with reset != 0, clear) the device status word of the current
  * device.  Synchronises `stream` first.  Returns FRT_OK, FRT_ETIMEOUT (some
- * bounded wait ran out since the last reset) or FRT_ECUDA. */
+ * bounded wait ran out since the last reset), FRT_ERANGE (some position, slot,
+ * page or length in device memory was out of range) or FRT_ECUDA.  The word
+ * holds the last of them that was recorded. */
 int frt_device_status(int reset, void* stream);
 
 /* ----------------------------------------------------------------------- */
@@ -469,6 +473,174 @@ int frt_style_project(int rows, int K, int N, const float* cond, long ld_cond,
                       const frt_bf16* w, long ldw, const float* bias,
                       frt_bf16* style_out, long ld_style, float* fin_out,
                       long ld_fin, int fin_col0, void* stream);
+
+/* ----------------------------------------------------------------------- */
+/* Rotary tables of scaled frequencies, per-head norms with rotation, the    */
+/* paged KV cache (bf16 or 4-bit pages) and attention over 4-bit pages.      */
+/* The pages of the source package have no counterpart; these stand beside   */
+/* frt_build_rope_table, frt_split_rope_kvcache and the dense caches.        */
+/* ----------------------------------------------------------------------- */
+
+enum {
+  FRT_ROPE_SCALE_NONE = 0,
+  FRT_ROPE_SCALE_LINEAR = 1, /* f_i / factor                                */
+  FRT_ROPE_SCALE_BASE = 2,   /* theta * factor^(rot / (rot - 2)) for theta  */
+  FRT_ROPE_SCALE_PARTS = 3   /* f_i (keep_i + (1 - keep_i) / factor) with
+                                keep_i = clamp((r_i - low_turns) /
+                                (high_turns - low_turns), 0, 1) and
+                                r_i = orig_len * f_i / (2 pi), the turns
+                                pair i makes over the trained context      */
+};
+
+/*
+ * frt_build_rope_table_scaled: for m < M, i < rot/2, f_i = theta^(-2i/rot)
+ * scaled as above,
+ *   rope[m, 2i] = fp32(amplitude * cos((P + m) * f_i)),  rope[m, 2i+1] = sin
+ * with the angle and the functions in fp64.  rope_out: device fp32 [M, rot],
+ * 8-byte aligned (frt_qk_rope_desc.rope wants 16).  rot even, 2 <= rot <=
+ * 65536; M, P >= 0; theta > 0; factor > 0, amplitude finite; rot > 2 for
+ * FRT_ROPE_SCALE_BASE; orig_len > 0 and high_turns > low_turns for
+ * FRT_ROPE_SCALE_PARTS (the three are ignored otherwise).  Within 1 ulp of
+ * the rounded fp64 value.  M == 0 is a no-op.
+ */
+int frt_build_rope_table_scaled(int M, int rot, long P, double theta, int scaling, double factor,
+                                double orig_len, double low_turns, double high_turns,
+                                double amplitude, float* rope_out, void* stream);
+
+enum {
+  FRT_ROPE_PAIRS = 0, /* rotates elements (2i, 2i + 1) of a head            */
+  FRT_ROPE_HALF = 1   /* rotates elements (i, rot/2 + i) of a head          */
+};
+enum {
+  FRT_PAGE_BF16 = 0,
+  FRT_PAGE_E2M1 = 1
+};
+
+/*
+ * Bytes of one page record: one kv head's page_size tokens.  A pool is one
+ * byte tensor [n_pages, hkv, record]; in a record, one after another,
+ *   FRT_PAGE_BF16: keys [page_size, hd] bf16, values [page_size, hd] bf16;
+ *   FRT_PAGE_E2M1: key codes [page_size, hd / 2] (e2m1, element 2j in the
+ *     low half of byte j), key scales [page_size, hd / 16] (e4m3), value
+ *     codes, value scales.
+ * An element of a 4-bit page is code * scale * (k_scale or v_scale).
+ * page_size: a power of two in [16, 1024]; hd: 16 .. 256, a multiple of 8
+ * (FRT_PAGE_BF16) or of 16 (FRT_PAGE_E2M1).  0 for anything else.
+ */
+size_t frt_kv_record_bytes(int format, int page_size, int hd);
+
+typedef struct frt_qk_rope_desc {
+  int rows;               /* tokens                                        */
+  int hq, hkv, hd;        /* a row of qkv: hq q heads, hkv k, hkv v heads   */
+  int rot, layout;        /* rotated leading elements (0 = none); FRT_ROPE_* */
+  float eps;              /* of the norms                                  */
+  const frt_bf16* qkv; long ld_qkv;   /* [rows, (hq + 2 hkv) * hd], strided */
+  const frt_bf16* q_norm; const frt_bf16* k_norm; /* [hd] or NULL = no norm */
+  const float* rope;      /* [n_pos, rot] fp32 (frt_build_rope_table_scaled) */
+  int n_pos;
+  const int* positions;   /* device [rows]: table row of each token;
+                             NULL = 0, 1, 2, ...                            */
+  frt_bf16* q_out; long ld_q;         /* [rows, hq * hd], strided           */
+  frt_bf16* k_out; long ld_k;         /* [rows, hkv * hd], strided          */
+  frt_bf16* v_out; long ld_v;         /* [rows, hkv * hd] (frt_paged_kv_read) */
+  /* the paged cache */
+  int format, page_size, n_pages;     /* FRT_PAGE_*                         */
+  void* pool;             /* [n_pages, hkv, record], 16-byte aligned        */
+  const long* slots;      /* device [rows]: page * page_size + row in the
+                             page; negative = no cache row for this token   */
+  const float* k_scale; const float* v_scale; /* device [1] (FRT_PAGE_E2M1) */
+} frt_qk_rope_desc;
+
+/*
+ * frt_qk_norm_rope: for every token and every q and k head x of its row,
+ * in fp32 (the mean square summed in fp64),
+ *   y = x / sqrt(mean(x^2) + eps) * norm      (q_norm / k_norm; NULL: y = x)
+ *   the first `rot` elements rotated in pairs (x0, x1) by the table's
+ *   (c, s): (x0 c - x1 s, x0 s + x1 c); the others kept; rounded once to bf16
+ * into q_out and k_out.  v is not read.  q_out / k_out may be the qkv rows
+ * themselves (q_out = qkv, k_out = qkv + hq * hd, ld = ld_qkv); any other
+ * overlap is not allowed.  The page fields and v_out are ignored.
+ * hd: 16 .. 256, a multiple of 8; rot: a multiple of 16, 0 <= rot <= hd; 16-
+ * byte aligned pointers and strides that are multiples of 8 and at least the
+ * row's width; hq or hkv may be 0, not both (k_out / q_out are then ignored).
+ * rows == 0 is a no-op.  A token whose position is outside [0, n_pos) is
+ * left out: its output rows keep what they held, and the device status word
+ * records FRT_ERANGE.
+ */
+int frt_qk_norm_rope(const frt_qk_rope_desc* d, void* stream);
+
+/*
+ * frt_paged_kv_append: the q and k heads as frt_qk_norm_rope, q into q_out
+ * (NULL: the q heads are skipped), and for every token with slot >= 0 the
+ * rotated k (rounded to bf16) and the v heads into the pool's pages.
+ * FRT_PAGE_E2M1 quantises each run of 16 elements x of a head: with y = x *
+ * (1 / k_scale) (v_scale for v; the reciprocal and the product rounded to
+ * fp32), scale = e4m3(min(max|y| / 6, 448)), code = e2m1(y / scale), both
+ * nearest-even and saturating; scale 0 gives codes 0.  A NaN element counts
+ * as 0 in max|y| and its code is a finite one.  k_out and v_out are ignored.  The slots
+ * of one call must be distinct (two tokens in one slot leave a mix of both).
+ * A slot >= n_pages * page_size is not written, and the status word records
+ * FRT_ERANGE; a bad position leaves the whole token out, as above.
+ * hkv >= 1; hd % 16 == 0 for FRT_PAGE_E2M1.
+ */
+int frt_paged_kv_append(const frt_qk_rope_desc* d, void* stream);
+
+/*
+ * frt_paged_kv_read: the cached rows at `slots` as bf16 into k_out and v_out
+ * (either may be NULL): the stored bf16 numbers, or bf16((code * scale) *
+ * k_scale).  Rows with a negative slot keep what they held; a slot past the
+ * pool likewise, with FRT_ERANGE in the status word.  Uses rows, hkv, hd,
+ * k_out, v_out and the page fields only.
+ */
+int frt_paged_kv_read(const frt_qk_rope_desc* d, void* stream);
+
+typedef struct frt_paged_attn_desc {
+  int n_seqs, rows;       /* sequences; rows of q and out                   */
+  int max_q;              /* most query rows of one sequence                */
+  int hq, hkv, hd;        /* hq a multiple of hkv; hd 64, 128 or 256        */
+  int page_size, max_pages, n_pages;
+  int causal, window;     /* window > 0: causal, the last `window` keys     */
+  float sm_scale;
+  const frt_bf16* q; long ld_q;       /* [rows, hq * hd], strided           */
+  const void* pool;       /* FRT_PAGE_E2M1 pool, 16-byte aligned            */
+  const int* page_table;  /* device [n_seqs, max_pages]                     */
+  const int* cu_rows;     /* device [n_seqs + 1]: sequence s has rows
+                             cu_rows[s] .. cu_rows[s + 1]; NULL = max_q each */
+  const int* kv_len;      /* device [n_seqs]: cached tokens, these queries'
+                             own among them                                 */
+  const float* k_scale; const float* v_scale; /* device [1]                 */
+  frt_bf16* out; long ld_out;         /* [rows, hq * hd], strided           */
+  float* lse;             /* [rows, hq] or NULL                             */
+  void* workspace; size_t workspace_bytes;
+} frt_paged_attn_desc;
+
+/* Workspace bytes frt_paged_attention_fp4 needs (current device); they
+ * depend on n_seqs, max_q, the heads and hd only, not on the lengths. */
+size_t frt_paged_attention_workspace_size(int n_seqs, int max_q, int hq, int hkv, int hd);
+
+/*
+ * frt_paged_attention_fp4: softmax attention of each sequence's query rows
+ * over its first kv_len cached tokens in 4-bit pages, key j of sequence s in
+ * row j % page_size of page page_table[s, j / page_size].  Query i of the
+ * sequence's Lq stands at place p = kv_len - Lq + i; with causal != 0 it
+ * sees keys j <= p, with window > 0 also j > p - window, else all keys.
+ *   out = sum_j softmax_j(sm_scale * q . k_j) v_j,  lse = log sum exp
+ * (natural logarithm); query head h reads kv head h / (hq / hkv).  A row that
+ * sees no key gives out = 0 and lse = -inf.  Rows outside every sequence keep
+ * what they held.  Products on the tensor cores with fp32 sums: the cached
+ * codes times their block scales are exact in fp16, q is scaled by a power
+ * of two into it, the weights are rounded to fp16 once; softmax statistics
+ * and sums in fp32; results are the same from call to call.
+ * workspace: zero-filled once before its first use; every completed call
+ * leaves its counters at zero.  Calls (and captured graphs) that share one
+ * must not overlap.  Only the pages that hold a sequence's first kv_len
+ * tokens are read; what the last page holds behind them does not matter.
+ * Device-side data that is out of range is never followed: a page id outside
+ * [0, n_pages) hides its tokens, kv_len is held to [0, max_pages *
+ * page_size], a sequence's rows to [0, rows] and its first max_q; each of
+ * these records FRT_ERANGE in the device status word.
+ */
+int frt_paged_attention_fp4(const frt_paged_attn_desc* d, void* stream);
 
 /* ----------------------------------------------------------------------- */
 /* Self-test of the bounded device wait.                                    */
