@@ -9,67 +9,31 @@
 // bits, 2^-10 .. 2688), so the cache is widened in registers to fp16 and the
 // products run on the tensor cores with fp32 sums; the static scales are
 // applied to the fp32 results.
-#include <cuda_fp16.h>
-
 #include <mutex>
 #include <set>
 #include <utility>
 
-#include "frt_paged.cuh"
-#include "frt_sm100.cuh"
+#include "frt_attn.cuh"
 
 namespace frt {
-namespace {
 
-constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s per wait
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-
-struct AttnArgs {
-  int n_seqs, rows, max_q, hq, hkv, group, causal, window;
-  int max_pages;
-  float sm_scale;
-  const uint16_t* q; long ld_q;
-  PagePool pool;
-  const int* page_table;
-  const int* cu_rows;
-  const int* kv_len;
-  const float* k_scale; const float* v_scale;
-  uint16_t* out; long ld_out;
-  float* lse;
-  int* counters;     // [grid], zero between calls
-  float* partials;   // [grid][2] tiles
-  int* status;
-};
-
-// One sequence: its query rows, its keys, and what its work is cut into.
-struct Seq {
-  int r0, Lq, L;        // first row, query rows, keys
-  int chunk0, chunks;   // the chunks any of its queries sees (one at least)
-  int tiles;            // row tiles of each kv head
-  __device__ long work(int hkv) const { return long(chunks) * hkv * tiles; }
-};
-
-template <int R, int CK>
-__device__ __forceinline__ Seq load_seq(const AttnArgs& a, int s, bool report) {
-  Seq q;
-  const long want0 = a.cu_rows ? a.cu_rows[s] : long(s) * a.max_q;
-  const long want1 = a.cu_rows ? a.cu_rows[s + 1] : long(s + 1) * a.max_q;
-  const long r0 = min(max(want0, 0L), long(a.rows));
-  const long r1 = min(min(max(want1, r0), long(a.rows)), r0 + a.max_q);
-  const long cap = long(a.max_pages) * a.pool.page_size;
-  const long want_l = a.kv_len[s];
-  const long L = min(max(want_l, 0L), cap);
-  if (report && (r0 != want0 || r1 != want1 || L != want_l)) atomicExch(a.status, FRT_ERANGE);
-  q.r0 = int(r0);
-  q.Lq = int(r1 - r0);
-  q.L = int(L);
-  q.tiles = (q.Lq * a.group + R - 1) / R;
-  const long first = a.window > 0 ? max(0L, L - q.Lq - a.window + 1) : 0;
-  q.chunk0 = int(first / CK);
-  q.chunks = max(1, int((L + CK - 1) / CK) - q.chunk0);
-  return q;
+// Before any thread's first launch of the kernel on the device.
+int allow_smem(const void* kern, int bytes) {
+  static std::mutex mu;
+  static std::set<std::pair<int, const void*>> done;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  std::lock_guard<std::mutex> lock(mu);
+  if (done.count({dev, kern})) return FRT_OK;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+    cudaGetLastError();
+    return fail(FRT_ECUDA, "frt_paged_attention_fp4: %d bytes of shared memory refused", bytes);
+  }
+  done.insert({dev, kern});
+  return FRT_OK;
 }
+
+namespace {
 
 // A position in the list of all (sequence, row tile, kv head, chunk).
 template <int R, int CK>
@@ -108,43 +72,6 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// The four bytes of w, two e2m1 codes each, as fp16 pairs.
-__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4]) {
-  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-      "mov.b32 {a, b, c, d}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(w));
-}
-
-// Two e4m3 codes (low byte first) as an fp16 pair.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t w) {
-  uint32_t h;
-  asm("{\n\t.reg .b16 x;\n\tcvt.u16.u32 x, %1;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, x;\n\t}" : "=r"(h) : "r"(w));
-  return h;
-}
-
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
 }
 
 template <int BYTES>
@@ -320,7 +247,7 @@ attn_few_kernel(AttnArgs a) {
       const uint32_t have = __ballot_sync(0xffffffffu, page >= 0);
       bool ok = true;
       if (lane == 0) {
-        ok = mbar_wait_bounded(&empty[stage], phase ^ 1u, kWaitNs, abort_flag);
+        ok = mbar_wait_bounded(&empty[stage], phase ^ 1u, kAttnWaitNs, abort_flag);
         if (!ok) {
           atomicExch(a.status, FRT_ETIMEOUT);
           *abort_flag = 1;
@@ -354,7 +281,7 @@ attn_few_kernel(AttnArgs a) {
     // after a wait that ran out: no exit with copies in flight
     if (*abort_flag && lane == 0) {
       for (long i = issued - C::kStages < 0 ? 0 : issued - C::kStages; i < issued; ++i)
-        mbar_wait_bounded(&full[i % C::kStages], uint32_t(i / C::kStages) & 1u, kWaitNs, nullptr);
+        mbar_wait_bounded(&full[i % C::kStages], uint32_t(i / C::kStages) & 1u, kAttnWaitNs, nullptr);
     }
     return;
   }
@@ -476,7 +403,7 @@ attn_few_kernel(AttnArgs a) {
     for (int n = 0; n < n_here; ++n, ++x) {
       const int key0 = (w.q.chunk0 + w.chunk + n) * CK + warp * 16;
       // every lane waits: each reads what the copies wrote
-      const bool got = mbar_wait_bounded(&full[stage], phase, kWaitNs, abort_flag);
+      const bool got = mbar_wait_bounded(&full[stage], phase, kAttnWaitNs, abort_flag);
       if (!got && lane == 0) {
         atomicExch(a.status, FRT_ETIMEOUT);
         *abort_flag = 1;
@@ -745,23 +672,6 @@ attn_few_kernel(AttnArgs a) {
 
 // ---------------------------------------------------------------- launch --
 
-// Opt a kernel into its shared memory on the current device, before any
-// thread's first launch of it there.
-int allow_smem(const void* kern, int bytes) {
-  static std::mutex mu;
-  static std::set<std::pair<int, const void*>> done;
-  int dev = 0;
-  cudaGetDevice(&dev);
-  std::lock_guard<std::mutex> lock(mu);
-  if (done.count({dev, kern})) return FRT_OK;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
-    cudaGetLastError();
-    return fail(FRT_ECUDA, "frt_paged_attention_fp4: %d bytes of shared memory refused", bytes);
-  }
-  done.insert({dev, kern});
-  return FRT_OK;
-}
-
 template <int HD, int NT>
 struct Few {
   using C = FewCfg<HD, NT>;
@@ -790,6 +700,9 @@ auto with_variant(int hd, long rows_per_head, F f) {
   return rows_per_head <= 8 ? f(Few<256, 1>{}) : f(Few<256, 2>{});
 }
 
+// Rows of one kv head from which the tensor-memory kernel takes over.
+bool many_rows(long rows_per_head) { return rows_per_head > 32; }
+
 bool head_counts_ok(int n_seqs, int max_q, int hq, int hkv, int hd) {
   return n_seqs >= 0 && max_q >= 0 && hkv >= 1 && hkv <= 65536 && hq >= hkv && hq <= 65536 &&
          hq % hkv == 0 && (hd == 64 || hd == 128 || hd == 256) &&
@@ -801,6 +714,8 @@ bool head_counts_ok(int n_seqs, int max_q, int hq, int hkv, int hd) {
 
 extern "C" size_t frt_paged_attention_workspace_size(int n_seqs, int max_q, int hq, int hkv, int hd) {
   if (!frt::head_counts_ok(n_seqs, max_q, hq, hkv, hd)) return 0;
+  if (frt::many_rows(long(max_q) * (hq / hkv)))
+    return frt::attn_many_workspace(hd, n_seqs, max_q, hq, hkv);
   return frt::with_variant(hd, long(max_q) * (hq / hkv), [](auto v) { return v.workspace(); });
 }
 
@@ -837,7 +752,7 @@ extern "C" int frt_paged_attention_fp4(const frt_paged_attn_desc* d, void* strea
               FRT_EALIGN, "page_table, cu_rows, kv_len, lse and the scales must be 4-byte aligned");
   const size_t need =
       frt_paged_attention_workspace_size(d->n_seqs, d->max_q, d->hq, d->hkv, d->hd);
-  FRT_REQUIRE(d->workspace, FRT_EINVAL, "workspace is required");
+  FRT_REQUIRE(d->workspace || need == 0, FRT_EINVAL, "workspace is required");
   FRT_REQUIRE(aligned(d->workspace, 16), FRT_EALIGN, "workspace must be 16-byte aligned");
   FRT_REQUIRE(d->workspace_bytes >= need, FRT_ERANGE, "workspace has %zu bytes, %zu needed",
               d->workspace_bytes, need);
@@ -854,6 +769,8 @@ extern "C" int frt_paged_attention_fp4(const frt_paged_attn_desc* d, void* strea
   a.status = frt::device_status_ptr();
   FRT_REQUIRE(a.status, FRT_ECUDA, "device status word unavailable");
   const long per_head = long(d->max_q) * a.group;
+  if (frt::many_rows(per_head))
+    return frt::attn_many_launch(a, d->hd, d->workspace, static_cast<cudaStream_t>(stream));
   return frt::with_variant(d->hd, per_head, [&](auto v) {
     using C = typename decltype(v)::C;
     const long tiles = (per_head + C::R - 1) / C::R;

@@ -1,0 +1,665 @@
+// paged_attn_many.cu -- attention over 4-bit pages for many query rows
+// (prompts, chunks): both products on tcgen05 tensor cores.
+//
+// A CTA takes R = 128 QT rows of one (sequence, kv head) -- row r is token
+// r / G, head r % G of the group -- and runs over their keys in tiles of KVT:
+//   S = Q K^T       Q fp16 (a power of two per row) and K fp16 in shared memory
+//   P = 2^(S - m)   written over S in tensor memory as fp16
+//   O += P V        P from tensor memory, V fp16 in shared memory
+// One thread owns one row of S and O, so the softmax needs no exchange
+// between threads.  The two row tiles of a CTA alternate: one's softmax runs
+// while the tensor cores work for the other.
+//
+// Bound by the tensor cores and the exponentials alike: a 128 x 128 tile of
+// hd 128 takes 2 x 512 clocks of MMA and 1024 of the 16-a-clock exponential
+// unit.  The widening of the codes is shared by all R rows (about a tenth of
+// the issue slots at R = 256), which is what the second row tile is for.
+//
+// When the units (sequences x heads x row tiles) leave SMs idle, the keys of
+// each are cut into `splits`, whose partial states a second kernel joins.
+#include "frt_attn.cuh"
+
+namespace frt {
+namespace {
+
+template <int HD>
+struct ManyCfg {
+  static constexpr int QT = HD == 256 ? 1 : 2;     // row tiles of 128
+  static constexpr int KVT = HD == 256 ? 64 : 128; // keys of a tile
+  static constexpr int R = 128 * QT;
+  static constexpr int kWide = HD == 256 ? 256 : 128;  // threads that widen codes
+  static constexpr int kThreads = 32 * 13;         // 4 QT softmax warps, the widening, the MMAs
+  static constexpr int kQBytes = 128 * HD * 2;     // one row tile
+  static constexpr int kKvBytes = KVT * HD * 2;    // one K or V tile
+  static constexpr int kBlock = KVT * 128;         // its 64-element column block
+  static constexpr int kSmem = QT * kQBytes + 4 * kKvBytes + 1024 + 256;
+  // TMEM columns: two S (or P) slots, then O
+  static constexpr int kTmem = 512;
+  static constexpr int kO = 2 * KVT;
+};
+
+// Instruction descriptor, kind::f16: D fp32 (bits 4-5 = 1), A and B f16
+// (0), A K-major, B K-major or MN-major (bit 16), N >> 3 at 17, M >> 4 at 24.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) {
+  return (1u << 4) | (b_mn_major ? 1u << 16 : 0u) | (uint32_t(N >> 3) << 17) |
+         (uint32_t(M >> 4) << 24);
+}
+
+// Shared-memory descriptor of an MN-major tile with the 128-byte swizzle:
+// atoms of 64 (contiguous) x 8 elements; `lead` bytes between atoms along the
+// contiguous dimension, 1024 bytes between groups of 8 along the other.
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t smem_addr, uint32_t lead) {
+  return uint64_t((smem_addr & 0x3FFFFu) >> 4) | (uint64_t(lead >> 4) << 16) |
+         (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+
+__device__ __forceinline__ void umma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+      :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+// A (128 rows x 16) from tensor memory: two f16 to a column, 8 columns.
+__device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      :: "r"(d), "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+// 32 columns of this thread's TMEM lane; the values may be used after
+// tmem_wait_ld(r).
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32"
+      " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15,"
+      " %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr) : "memory");
+}
+
+// The registers pass through the wait, so no use can move ahead of it.
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.wait::ld.sync.aligned;"
+      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+        "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
+        "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]),
+        "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]),
+        "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+      :: "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0],"
+      " {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+      :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+         "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
+         "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// The key tiles [begin, end) that row tile rows [row0, row0 + 128) sees.
+template <int KVT>
+__device__ __forceinline__ void tile_range(const AttnArgs& a, const Seq& q, int row0, int* begin,
+                                           int* end) {
+  const int rows = q.Lq * a.group;
+  *begin = *end = 0;
+  if (row0 >= rows) return;
+  const int first = q.L - q.Lq + row0 / a.group;
+  const int last = q.L - q.Lq + min(row0 + 127, rows - 1) / a.group;
+  const int hi = a.causal ? min(q.L, last + 1) : q.L;
+  const int lo = a.window > 0 ? max(0, first - a.window + 1) : 0;
+  if (hi <= lo) return;
+  *begin = lo / KVT;
+  *end = (hi + KVT - 1) / KVT;
+}
+
+// Partial states: [unit * splits + split] tiles of R rows x HD sums, then
+// the rows' maxima and sums of weights.
+template <int HD>
+__device__ __forceinline__ float* partial_tile(float* base, long index) {
+  return base + index * (ManyCfg<HD>::R * (HD + 2));
+}
+
+template <int HD>
+__global__ void __launch_bounds__(ManyCfg<HD>::kThreads, 1)
+attn_many_kernel(AttnArgs a, int splits, int tiles_max) {
+  using C = ManyCfg<HD>;
+  constexpr int QT = C::QT, KVT = C::KVT, R = C::R;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + (1024 - smem_u32(smem_raw) % 1024) % 1024;
+  uint8_t* q_s = smem;
+  uint8_t* k_s = q_s + QT * C::kQBytes;
+  uint8_t* v_s = k_s + 2 * C::kKvBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(v_s + 2 * C::kKvBytes);
+  uint64_t *q_full = bars, *k_full = bars + 2, *k_empty = bars + 4, *v_full = bars + 6,
+           *v_empty = bars + 8, *s_full = bars + 10, *p_full = bars + 12, *pv_done = bars + 14,
+           *done = bars + 16;
+  uint32_t* k_hidden = reinterpret_cast<uint32_t*>(bars + 17);  // [4] 16-key groups in bad pages
+  uint32_t* tmem_ptr = k_hidden + 4;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(k_hidden + 5);
+
+  const int tid = int(threadIdx.x), warp = tid / 32, lane = tid % 32;
+  pdl_trigger();
+  pdl_wait();
+  long b = blockIdx.x;
+  const long part_index = b;
+  const int split = int(b % splits);
+  b /= splits;
+  const int head = int(b % a.hkv);
+  b /= a.hkv;
+  const int s = int(b % a.n_seqs);
+  // causal tiles with the most keys first
+  const int tile = tiles_max - 1 - int(b / a.n_seqs);
+  const Seq q = load_seq<R, KVT>(a, s, tile == 0 && head == 0 && split == 0 && tid == 0);
+  if (tile >= q.tiles) return;
+
+  int begin[QT], end[QT], lo = 0x7fffffff, hi = 0;
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    tile_range<KVT>(a, q, tile * R + t * 128, &begin[t], &end[t]);
+    if (begin[t] < end[t]) {
+      lo = min(lo, begin[t]);
+      hi = max(hi, end[t]);
+    }
+  }
+  const int n_all = max(0, hi - lo);
+  const int js = lo + int(long(n_all) * split / splits), je = lo + int(long(n_all) * (split + 1) / splits);
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    begin[t] = max(begin[t], js);
+    end[t] = min(end[t], je);
+  }
+  const int n = n_all ? je - js : 0;
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 128);
+      mbar_init(&k_full[i], C::kWide);
+      mbar_init(&v_full[i], C::kWide);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_empty[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 128);
+      mbar_init(&pv_done[i], 1);
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 12) {
+    tmem_alloc(tmem_ptr, C::kTmem);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_ptr;
+
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (mbar_wait_bounded(bar, parity, kAttnWaitNs, abort_flag)) return true;
+    atomicExch(a.status, FRT_ETIMEOUT);
+    *abort_flag = 1;
+    return false;
+  };
+  // one answer for the warp, whose next steps are warp-wide
+  auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait(bar, parity)) != 0;
+  };
+
+  if (warp < 4 * QT) {
+    // ------------------------------------------------- softmax, one row ----
+    const int t = warp / 4, r = tid % 128;
+    const int row = tile * R + t * 128 + r;
+    const bool live = row < q.Lq * a.group;
+    const int token = live ? row / a.group : 0;
+    const int h = head * a.group + (live ? row - token * a.group : 0);
+    const uint32_t lane_base = tmem + (uint32_t(warp % 4 * 32) << 16);
+
+    // Q: fp16 under a power of two that brings the row's largest below 2
+    const uint16_t* src = a.q + long(q.r0 + token) * a.ld_q + long(h) * HD;
+    float big = 0.0f;
+    if (live) {
+#pragma unroll 8
+      for (int i = 0; i < HD / 8; ++i) {
+        float f[8];
+        unpack8(reinterpret_cast<const uint4*>(src)[i], f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) big = fmaxf(big, fabsf(f[k]));
+      }
+    }
+    int e = int(__float_as_uint(big) >> 23);
+    if (e < 1 || e > 253) e = 127;
+    // the sign of the scale goes into Q, so that the largest score is that of
+    // the largest product
+    const float scale = *a.k_scale * a.sm_scale * kLog2e;
+    const float down = copysignf(__uint_as_float(uint32_t(254 - e) << 23), scale);
+    const float c = fabsf(scale) * __uint_as_float(uint32_t(e) << 23);
+#pragma unroll 8
+    for (int i = 0; i < HD / 8; ++i) {
+      float f[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+      if (live) unpack8(reinterpret_cast<const uint4*>(src)[i], f);
+      const uint4 o = make_uint4(pack_f16x2(f[0] * down, f[1] * down), pack_f16x2(f[2] * down, f[3] * down),
+                                 pack_f16x2(f[4] * down, f[5] * down), pack_f16x2(f[6] * down, f[7] * down));
+      *reinterpret_cast<uint4*>(q_s + t * C::kQBytes + i / 8 * (128 * 128) + r * 128 +
+                                ((i % 8) ^ (r & 7)) * 16) = o;
+    }
+    fence_proxy_async_smem();
+    mbar_arrive(&q_full[t]);
+
+    int lim_hi = 0, lim_lo = 0;
+    if (live) {
+      const int place = q.L - q.Lq + token;
+      lim_hi = a.causal ? min(q.L, place + 1) : q.L;
+      lim_lo = a.window > 0 ? max(0, place - a.window + 1) : 0;
+    }
+    float m = -INFINITY;
+    uint64_t l2 = 0;
+    int k = 0;
+    const uint64_t c2 = f2_pack(c, c);
+    for (int j = begin[t]; j < end[t]; ++j, ++k) {
+      const int slot = QT == 2 ? t : k & 1;
+      if (!wait_warp(&s_full[slot], QT == 2 ? k & 1 : (k >> 1) & 1)) break;
+      tc_fence_after();
+      const uint32_t s_addr = lane_base + slot * KVT;
+      const uint32_t hidden = k_hidden[(j - js) & 3];
+      const int key0 = j * KVT;
+      const int rel_hi = lim_hi - key0, rel_lo = lim_lo - key0;
+      const bool masked = __any_sync(0xffffffffu, rel_hi < KVT || rel_lo > 0) || hidden;
+      // drop what the row does not see from 32 scores
+      auto mask32 = [&](uint32_t (&x)[32], int base) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const bool out = base + i >= rel_hi || base + i < rel_lo || (hidden >> ((base + i) / 16) & 1);
+          if (out) x[i] = 0xFF800000u;  // -inf
+        }
+      };
+
+      // the row's largest product
+      float mx = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < KVT / 32; ++i) {
+        uint32_t x[32];
+        tmem_ld32_async(s_addr + 32 * i, x);
+        tmem_wait_ld(x);
+        if (masked) mask32(x, 32 * i);
+#pragma unroll
+        for (int u = 0; u < 32; u += 2)
+          mx = fmaxf(fmaxf(mx, __uint_as_float(x[u])), __uint_as_float(x[u + 1]));
+      }
+      const float top = mx == -INFINITY ? mx : mx * c;
+      // the maximum is raised only when a score passes it by more than 2^8
+      // (the weights then stay within fp16), so O is rarely rescaled
+      const bool grow = top > m + 8.0f;
+      if (__any_sync(0xffffffffu, grow)) {
+        const float f = grow ? ex2(m - top) : 1.0f;
+        l2 = mul2(l2, f2_pack(f, f));
+        if (grow) m = top;
+        if (k > 0) {
+          // S of tile k vouches for the products up to k - 2, and those of
+          // k wait for this warp: the parity names those of k - 1
+          if (!wait_warp(&pv_done[t], (k - 1) & 1)) break;
+          tc_fence_after();
+#pragma unroll
+          for (int i = 0; i < HD / 32; ++i) {
+            uint32_t x[32];
+            tmem_ld32_async(lane_base + C::kO + t * HD + 32 * i, x);
+            tmem_wait_ld(x);
+#pragma unroll
+            for (int u = 0; u < 32; ++u) x[u] = __float_as_uint(__uint_as_float(x[u]) * f);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              uint32_t y[16];
+#pragma unroll
+              for (int w = 0; w < 16; ++w) y[w] = x[16 * u + w];
+              tmem_st16(lane_base + C::kO + t * HD + 32 * i + 16 * u, y);
+            }
+          }
+          tmem_wait_st();
+        }
+      }
+      const float base = m == -INFINITY ? 0.0f : -m;
+      const uint64_t base2 = f2_pack(base, base);
+#pragma unroll
+      for (int i = 0; i < KVT / 32; ++i) {
+        uint32_t x[32], p[16];
+        tmem_ld32_async(s_addr + 32 * i, x);
+        tmem_wait_ld(x);
+        if (masked) mask32(x, 32 * i);
+#pragma unroll
+        for (int u = 0; u < 16; ++u) {
+          const uint64_t v = fma2(f2_pack(__uint_as_float(x[2 * u]), __uint_as_float(x[2 * u + 1])), c2, base2);
+          const float p0 = ex2(f2_lo(v)), p1 = ex2(f2_hi(v));
+          l2 = add2(l2, f2_pack(p0, p1));
+          p[u] = pack_f16x2(p0, p1);
+        }
+        tmem_st16(s_addr + 16 * i, p);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&p_full[slot]);
+    }
+
+    // --- the row's result ---
+    const float l = f2_lo(l2) + f2_hi(l2);
+    const bool whole = splits == 1;
+    float* part = partial_tile<HD>(a.partials, part_index);
+    const float inv = l > 0.0f ? *a.v_scale / l : l * *a.v_scale;
+    if (k > 0 && !wait_warp(done, 0)) k = 0;  // every product issued is in
+    tc_fence_after();
+#pragma unroll 1
+    for (int i = 0; i < HD / 32; ++i) {
+      uint32_t x[32];
+      if (k > 0) {
+        tmem_ld32_async(lane_base + C::kO + t * HD + 32 * i, x);
+        tmem_wait_ld(x);
+      } else {
+#pragma unroll
+        for (int u = 0; u < 32; ++u) x[u] = 0;
+      }
+      if (live && whole) {
+        uint4* dst = reinterpret_cast<uint4*>(a.out + long(q.r0 + token) * a.ld_out + long(h) * HD + 32 * i);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          float f[8];
+#pragma unroll
+          for (int w = 0; w < 8; ++w) f[w] = __uint_as_float(x[8 * u + w]) * inv;
+          dst[u] = pack8_bf16(f);
+        }
+      } else if (live) {
+        float4* dst = reinterpret_cast<float4*>(part + long(t * 128 + r) * HD + 32 * i);
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          dst[u] = make_float4(__uint_as_float(x[4 * u]), __uint_as_float(x[4 * u + 1]),
+                               __uint_as_float(x[4 * u + 2]), __uint_as_float(x[4 * u + 3]));
+      }
+      __syncwarp();
+    }
+    if (live && whole && a.lse)
+      a.lse[long(q.r0 + token) * a.hq + h] = m == -INFINITY ? m : (m + log2f(l)) * kLn2;
+    if (!whole) {
+      part[R * HD + t * 128 + r] = m;
+      part[R * HD + R + t * 128 + r] = l;
+    }
+  } else if (warp < 12) {
+    // ------------------------------------------- widening, K then V tiles ----
+    const int wt = tid - (12 * 32 - C::kWide);
+    constexpr int kPieces = KVT * HD / 32;       // 32 codes and two scales
+    constexpr int kMine = kPieces / C::kWide;
+    const int ps = a.pool.page_size;
+    uint4 code[kMine];
+    uint32_t scl[kMine];
+    auto load = [&](int j, int half) {           // half 0: keys, 1: values
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const int flat = i * C::kWide + wt;
+        const int key = j * KVT + flat / (HD / 32), piece = flat % (HD / 32);
+        code[i] = make_uint4(0, 0, 0, 0);
+        scl[i] = 0;
+        if (key < q.L) {
+          const int page = a.page_table[long(s) * a.max_pages + (key >> a.pool.shift)];
+          if (page >= 0 && page < a.pool.n_pages) {
+            const int at = key & (ps - 1);
+            const uint8_t* rec = a.pool.base + (long(page) * a.pool.hkv + head) * a.pool.record_bytes +
+                                 half * (a.pool.record_bytes / 2);
+            code[i] = __ldg(reinterpret_cast<const uint4*>(rec + at * (HD / 2) + piece * 16));
+            scl[i] = __ldg(reinterpret_cast<const uint16_t*>(rec + ps * (HD / 2) + at * (HD / 16) + piece * 2));
+          }
+        }
+      }
+    };
+    auto widen = [&](uint8_t* dst) {
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const int flat = i * C::kWide + wt;
+        const int key = flat / (HD / 32), piece = flat % (HD / 32);
+        uint32_t sc = e4m3x2_to_f16(scl[i]);
+        uint8_t* rowp = dst + piece / 2 * C::kBlock + key * 128;
+        uint32_t w[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
+        // eight neighbouring lanes write eight different 16-byte columns:
+        // pieces of different column blocks start at different words
+        const int turn = HD == 256 ? piece / 2 : HD == 128 ? piece / 2 * 2 : 0;
+        if (HD >= 128 && (turn & 2)) {
+          uint32_t x = w[0]; w[0] = w[2]; w[2] = x;
+          x = w[1]; w[1] = w[3]; w[3] = x;
+          sc = __byte_perm(sc, 0, 0x1032);
+        }
+        if (HD == 256 && (turn & 1)) {
+          uint32_t x = w[0]; w[0] = w[1]; w[1] = x;
+          x = w[2]; w[2] = w[3]; w[3] = x;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          uint32_t hv[4];
+          e2m1x8_to_f16(w[u], hv);
+          const uint32_t s2 = __byte_perm(sc, 0, u < 2 ? 0x1010 : 0x3232);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) hv[v] = hmul2(hv[v], s2);
+          const int col = (piece % 2 * 4 + (u ^ turn)) ^ (key & 7);
+          *reinterpret_cast<uint4*>(rowp + col * 16) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
+        }
+      }
+      fence_proxy_async_smem();
+    };
+    if (n > 0) load(js, 0);
+    for (int i = 0; i < n; ++i) {
+      const int st = i & 1;
+      const uint32_t ph = (i >> 1) & 1;
+      if (!wait_warp(&k_empty[st], ph ^ 1u)) break;
+      if (wt < 32) {  // one warp looks the tile's pages over for the mask
+        const int key = (js + i) * KVT + lane * 16;
+        bool bad = false;
+        if (lane < KVT / 16 && key < q.L) {
+          const int page = a.page_table[long(s) * a.max_pages + (key >> a.pool.shift)];
+          bad = page < 0 || page >= a.pool.n_pages;
+          if (bad) atomicExch(a.status, FRT_ERANGE);
+        }
+        const uint32_t mask = __ballot_sync(0xffffffffu, bad);
+        if (lane == 0) k_hidden[i & 3] = mask;
+      }
+      widen(k_s + st * C::kKvBytes);
+      mbar_arrive(&k_full[st]);
+      load(js + i, 1);
+      if (!wait_warp(&v_empty[st], ph ^ 1u)) break;
+      widen(v_s + st * C::kKvBytes);
+      mbar_arrive(&v_full[st]);
+      if (i + 1 < n) load(js + i + 1, 0);
+    }
+  } else if (tid == 12 * 32) {
+    // ------------------------------------------------------------ the MMAs ----
+    constexpr uint32_t kQk = idesc_f16(128, KVT, false);
+    constexpr uint32_t kPv = idesc_f16(128, HD, true);
+    const uint32_t qa = smem_u32(q_s), ka = smem_u32(k_s), va = smem_u32(v_s);
+    auto qk = [&](int t, int slot, int st) {
+#pragma unroll
+      for (int kk = 0; kk < HD / 16; ++kk) {
+        const uint32_t off = kk % 4 * 32;
+        umma_f16_ss(tmem + slot * KVT, sdesc_k_sw128(qa + t * C::kQBytes + kk / 4 * (128 * 128) + off),
+                    sdesc_k_sw128(ka + st * C::kKvBytes + kk / 4 * C::kBlock + off), kQk, kk > 0);
+      }
+      umma_commit(&s_full[slot]);
+    };
+    auto pv = [&](int t, int slot, int st, bool more) {
+#pragma unroll
+      for (int kk = 0; kk < KVT / 16; ++kk)
+        umma_f16_ts(tmem + C::kO + t * HD, tmem + slot * KVT + 8 * kk,
+                    sdesc_mn_sw128(va + st * C::kKvBytes + kk * 2048, C::kBlock), kPv, more || kk > 0);
+      umma_commit(&pv_done[t]);
+    };
+    bool ok = true;
+    int k[QT];     // tiles done by a row tile
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+      k[t] = 0;
+      if (n > 0) ok = ok && wait(&q_full[t], 0);
+    }
+    if constexpr (QT == 2) {
+      // at tile j, for each row tile: P V of tile j - 1 (its P overlies the
+      // S of tile j), then Q K^T of tile j
+      bool pending[2] = {false, false};
+      for (int i = 0; ok && i <= n; ++i) {
+        const int st = i & 1, j = js + i;
+        if (i < n) ok = wait(&k_full[st], (i >> 1) & 1);
+        tc_fence_after();
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (ok && pending[t]) {
+            ok = wait(&v_full[st ^ 1], ((i - 1) >> 1) & 1) && wait(&p_full[t], (k[t] - 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            pv(t, t, st ^ 1, k[t] > 1);
+            pending[t] = false;
+          }
+          if (ok && i < n && j >= begin[t] && j < end[t]) {
+            qk(t, t, st);
+            pending[t] = true;
+            ++k[t];
+          }
+        }
+        if (ok && i > 0) umma_commit(&v_empty[st ^ 1]);
+        if (ok && i < n) umma_commit(&k_empty[st]);
+      }
+    } else {
+      // two S slots: Q K^T of tile j before P V of tile j - 1
+      for (int i = 0; ok && i <= n; ++i) {
+        const int st = i & 1;
+        if (i < n) {
+          ok = wait(&k_full[st], (i >> 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          qk(0, st, st);
+          umma_commit(&k_empty[st]);
+        }
+        if (i > 0) {
+          const uint32_t ph = ((i - 1) >> 1) & 1;
+          ok = wait(&v_full[st ^ 1], ph) && wait(&p_full[st ^ 1], ph);
+          if (!ok) break;
+          tc_fence_after();
+          pv(0, st ^ 1, st ^ 1, i > 1);
+          umma_commit(&v_empty[st ^ 1]);
+        }
+      }
+    }
+    // nothing in flight when the tensor memory is freed
+    umma_commit(done);
+    mbar_wait_bounded(done, 0, kAttnWaitNs, nullptr);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 12) tmem_dealloc(tmem, C::kTmem);
+}
+
+// Joins the splits: one warp a row and head.
+template <int HD>
+__global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, int splits, int tiles_max) {
+  using C = ManyCfg<HD>;
+  constexpr int V = HD / 32;  // floats a lane
+  const int lane = int(threadIdx.x) % 32;
+  const long w = (blockIdx.x * 256L + threadIdx.x) / 32;
+  pdl_trigger();
+  pdl_wait();
+  const long per_seq = long(a.max_q) * a.hq;
+  const int s = int(w / per_seq);
+  if (s >= a.n_seqs) return;
+  const int token = int(w % per_seq / a.hq), h = int(w % a.hq);
+  const Seq q = load_seq<C::R, C::KVT>(a, s, false);
+  if (token >= q.Lq) return;
+  const int head = h / a.group;
+  const int row = token * a.group + h - head * a.group;
+  const long unit = (long(tiles_max - 1 - row / C::R) * a.n_seqs + s) * a.hkv + head;
+  const int r = row % C::R;
+  float m = -INFINITY;
+  for (int i = 0; i < splits; ++i)
+    m = fmaxf(m, partial_tile<HD>(a.partials, unit * splits + i)[C::R * HD + r]);
+  float l = 0.0f, acc[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) acc[v] = 0.0f;
+  for (int i = 0; i < splits; ++i) {
+    const float* p = partial_tile<HD>(a.partials, unit * splits + i);
+    const float mi = p[C::R * HD + r];
+    if (mi == -INFINITY) continue;   // a share of the keys that the row does not see
+    const float f = ex2(mi - m);
+    l += p[C::R * HD + C::R + r] * f;
+#pragma unroll
+    for (int v = 0; v < V; v += 2) {
+      const float2 x = *reinterpret_cast<const float2*>(p + long(r) * HD + (v / 2 * 32 + lane) * 2);
+      acc[v] += x.x * f;
+      acc[v + 1] += x.y * f;
+    }
+  }
+  const float inv = l > 0.0f ? *a.v_scale / l : l * *a.v_scale;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + long(q.r0 + token) * a.ld_out + long(h) * HD);
+#pragma unroll
+  for (int v = 0; v < V; v += 2) dst[v / 2 * 32 + lane] = pack_bf16x2(acc[v] * inv, acc[v + 1] * inv);
+  if (lane == 0 && a.lse)
+    a.lse[long(q.r0 + token) * a.hq + h] = m == -INFINITY ? m : (m + log2f(l)) * kLn2;
+}
+
+template <int HD>
+struct Many {
+  using C = ManyCfg<HD>;
+  static long tiles(int max_q, int group) { return (long(max_q) * group + C::R - 1) / C::R; }
+  static long units(int n_seqs, int max_q, int hq, int hkv) {
+    return long(n_seqs) * hkv * tiles(max_q, hq / hkv);
+  }
+  // As many splits as the idle SMs hold, 16 at most.
+  static int splits(int n_seqs, int max_q, int hq, int hkv) {
+    const long u = units(n_seqs, max_q, hq, hkv);
+    const long n = u > 0 ? num_sms() / u : 1;
+    return n < 1 ? 1 : n > 16 ? 16 : int(n);
+  }
+  static size_t workspace(int n_seqs, int max_q, int hq, int hkv) {
+    const int n = splits(n_seqs, max_q, hq, hkv);
+    return n == 1 ? 0 : size_t(units(n_seqs, max_q, hq, hkv)) * n * C::R * (HD + 2) * 4;
+  }
+  static int launch(AttnArgs a, void* ws, cudaStream_t st) {
+    auto kern = attn_many_kernel<HD>;
+    if (int rc = allow_smem(reinterpret_cast<const void*>(kern), C::kSmem)) return rc;
+    // two key tiles a split at least
+    const long key_tiles = (long(a.max_pages) * a.pool.page_size + C::KVT - 1) / C::KVT;
+    int n = splits(a.n_seqs, a.max_q, a.hq, a.hkv);
+    if (n > 1 && n > key_tiles / 2) n = key_tiles < 2 ? 1 : int(key_tiles / 2);
+    a.partials = static_cast<float*>(ws);
+    const int tm = int(tiles(a.max_q, a.group));
+    const long blocks = units(a.n_seqs, a.max_q, a.hq, a.hkv) * n;
+    FRT_REQUIRE(blocks <= 0x7fffffffL, FRT_ESHAPE, "n_seqs * max_q * hq is too large");
+    if (int rc = launch_pdl("frt_paged_attention_fp4", kern, dim3(unsigned(blocks)), dim3(C::kThreads),
+                            C::kSmem, st, a, n, tm))
+      return rc;
+    if (n == 1) return FRT_OK;
+    const long warps = long(a.n_seqs) * a.max_q * a.hq;
+    return launch_pdl("frt_paged_attention_fp4", attn_join_kernel<HD>, dim3(unsigned((warps + 7) / 8)),
+                      dim3(256), 0, st, a, n, tm);
+  }
+};
+
+}  // namespace
+
+size_t attn_many_workspace(int hd, int n_seqs, int max_q, int hq, int hkv) {
+  return hd == 64    ? Many<64>::workspace(n_seqs, max_q, hq, hkv)
+         : hd == 128 ? Many<128>::workspace(n_seqs, max_q, hq, hkv)
+                     : Many<256>::workspace(n_seqs, max_q, hq, hkv);
+}
+
+int attn_many_launch(const AttnArgs& a, int hd, void* workspace, cudaStream_t stream) {
+  return hd == 64    ? Many<64>::launch(a, workspace, stream)
+         : hd == 128 ? Many<128>::launch(a, workspace, stream)
+                     : Many<256>::launch(a, workspace, stream);
+}
+
+}  // namespace frt

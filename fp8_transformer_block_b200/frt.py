@@ -174,8 +174,9 @@ def ptr(x):
 
 def _stream(stream):
     if stream is None:
+        # the raw handle: building a Stream object costs as much as a launch
         import torch
-        return torch.cuda.current_stream().cuda_stream or None
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) or None
     if isinstance(stream, int):
         return stream or None
     return stream.cuda_stream or None

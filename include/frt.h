@@ -631,7 +631,7 @@ size_t frt_paged_attention_workspace_size(int n_seqs, int max_q, int hq, int hkv
  * codes times their block scales are exact in fp16, q is scaled by a power
  * of two into it, the weights are rounded to fp16 once; softmax statistics
  * and sums in fp32; results are the same from call to call.
- * workspace: zero-filled once before its first use; every completed call
+ * workspace (NULL where the size is 0): zero-filled once before its first use; every completed call
  * leaves its counters at zero.  Calls (and captured graphs) that share one
  * must not overlap.  Only the pages that hold a sequence's first kv_len
  * tokens are read; what the last page holds behind them does not matter.

@@ -74,15 +74,18 @@ class Problem:
         max_q = max(1, max(q for q, _ in lens))
         self.nbytes = frt.frt_paged_attention_workspace_size(n, max_q, hq, hkv, hd)
         self.ws = runtime.workspace(self.nbytes)
+        self.counters = max_q * hq // hkv <= 32   # the kernels for few rows keep counters
         self.d = runtime.paged_attn_desc(
             n_seqs=n, rows=self.rows, max_q=max_q, hq=hq, hkv=hkv, hd=hd, page_size=ps, max_pages=self.max_pages,
             n_pages=self.n_pages, causal=int(causal), window=window, sm_scale=self.scale, ld_q=hq * hd + pad,
             ld_out=hq * hd + pad, out=self.out, lse=self.lse, workspace=self.ws, workspace_bytes=self.nbytes, **self.t)
 
-    def run(self, stream=None):
+    def run(self, stream=None, report=True):
         frt, runtime, torch = self.rt
         frt.frt_paged_attention_fp4(self.d, stream=stream)
         torch.cuda.synchronize()
+        if report:
+            assert frt.frt_device_status(True) == frt.FRT_OK
 
     def results(self):
         frt, runtime, torch = self.rt
@@ -111,7 +114,8 @@ class Problem:
                 assert np.all(np.abs(g[~empty] - wl[~empty]) <= tl[~empty])
         assert np.all(o[self.cu[-1]:] == 5.0) and np.all(o[:, w:] == 5.0)
         assert lse is None or np.all(lse[self.cu[-1]:] == 5.0)
-        assert int(self.ws[:4096].view(torch.int32)[:148].abs().sum()) == 0
+        if self.counters:
+            assert int(self.ws[:4 * 148].view(torch.int32).abs().sum()) == 0
 
 
 LENGTHS = [1, 2, 15, 16, 17, 31, 63, 64, 65, 127, 128, 129, 255, 257, 500, 1025]
@@ -216,7 +220,7 @@ def test_indices_out_of_range(rt, max_q):
     p = Problem(rt, rng, [(Lq, 600), (Lq, 300)], 4, 1, 64, 64, causal=False)
     for bad in (-1, p.n_pages, 2 ** 31 - 1):
         p.t["page_table"][0, 3] = bad
-        p.run()
+        p.run(report=False)
         assert frt.frt_device_status(True) == frt.FRT_ERANGE
         keep = np.r_[0:192, 256:600]
         k, v = p.kv[0]
@@ -226,11 +230,11 @@ def test_indices_out_of_range(rt, max_q):
         assert np.all(np.abs(got - want) <= ref.HALF_BF16 * np.abs(want) + tol)
         p.check(only=[1])
     p.t["page_table"].copy_(torch.from_numpy(p.table))
-    p.run()
+    p.run(report=False)
     assert frt.frt_device_status(True) == frt.FRT_OK
     p.check()
     p.t["kv_len"][1] = -5
-    p.run()
+    p.run(report=False)
     assert frt.frt_device_status(True) == frt.FRT_ERANGE
     o, lse = p.results()
     assert np.all(o[Lq:2 * Lq] == 0) and np.all(np.isneginf(lse[Lq:2 * Lq]))
@@ -240,13 +244,13 @@ def test_indices_out_of_range(rt, max_q):
         p.t["cu_rows"].copy_(torch.tensor(cu, dtype=torch.int32))
         p.out.fill_(5.0)
         p.lse.fill_(5.0)
-        p.run()
+        p.run(report=False)
         assert frt.frt_device_status(True) == frt.FRT_ERANGE
         p.check(only=[0]) if cu[0] == 0 and cu[1] == Lq and cu[2] > 0 else None
     p.t["cu_rows"].copy_(torch.tensor([0, Lq, 2 * Lq], dtype=torch.int32))
     p.out.fill_(5.0)
     p.lse.fill_(5.0)
-    p.run()
+    p.run(report=False)
     assert frt.frt_device_status(True) == frt.FRT_OK
     p.check()
 
