@@ -3,8 +3,8 @@
 // 4-bit pages).
 //
 // All of it is bound by bytes: a head of a row is read once, in 16-byte
-// pieces of 8 elements held by neighbouring lanes, normed, rotated and
-// written (or quantised into its page) from registers.  See the kernels.
+// pieces of 8 elements, normed, rotated and written (or quantised into its
+// page) from registers.  See the kernels.
 #include <cuda_fp4.h>
 #include <math.h>
 
@@ -18,16 +18,22 @@ namespace {
 struct TableArgs {
   int M, rot, scaling, steps;
   long P;
-  double theta, factor, orig_len, low, high, amplitude;
+  double log2_base, log2_base_lo;  // of the (scaled) base, in two parts
+  double factor, orig_len, low, high, amplitude;
   float* out;
 };
 
-// f_i of the header's formula.
-__device__ double scaled_frequency(const TableArgs& a, int i) {
+// f_i of the header's formula.  base^(-2i/rot) = 2^(e L): the rounding of the
+// exponent e = -2i/rot and of its product with L (up to 2^5) would cost a
+// few bits, so both are carried in two parts.
+__device__ __forceinline__ double scaled_frequency(const TableArgs& a, int i) {
   const double e = -2.0 * i / a.rot;
-  double f = pow(a.theta, e);
+  const double e_lo = fma(-e, double(a.rot), -2.0 * i) / a.rot;
+  const double x = e * a.log2_base;
+  const double x_lo = fma(e, a.log2_base, -x) + (e * a.log2_base_lo + e_lo * a.log2_base);
+  double f = exp2(x);
+  f = fma(f, x_lo * 0.693147180559945309417, f);
   if (a.scaling == FRT_ROPE_SCALE_LINEAR) f /= a.factor;
-  if (a.scaling == FRT_ROPE_SCALE_BASE) f *= pow(a.factor, e * (double(a.rot) / (a.rot - 2)));
   if (a.scaling == FRT_ROPE_SCALE_PARTS) {
     const double turns = a.orig_len * f / 6.283185307179586476925;
     const double keep = fmin(fmax((turns - a.low) / (a.high - a.low), 0.0), 1.0);
@@ -36,22 +42,43 @@ __device__ double scaled_frequency(const TableArgs& a, int i) {
   return f;
 }
 
-// One thread per (pair i, run of `steps` positions): cos and sin of the run's
-// first angle and of the frequency itself in fp64.
-__global__ void rope_table_scaled_kernel(TableArgs a) {
+// One thread per (pair i, run of `steps` positions).  cos and sin of the
+// run's middle angle and of one step are evaluated in fp64; the others
+// follow by the addition theorem, outwards in both directions: at most
+// steps/2 <= 16 complex products, 2^-53 each, against the 2^-24 of the fp32
+// result.  Bound: bytes for long tables (the fp64 evaluation is shared by the
+// run), the latency of exp2 and sincos for short ones.
+__global__ void __launch_bounds__(256) rope_table_scaled_kernel(TableArgs a) {
   const int half = a.rot / 2;
-  const long runs = (long(a.M) + a.steps - 1) / a.steps;
-  const long g = blockIdx.x * long(blockDim.x) + threadIdx.x;
-  if (g >= runs * half) return;
-  const int i = int(g % half);
-  const long m0 = g / half * a.steps;
+  const long g = blockIdx.x * 256L + threadIdx.x;
+  const long run = g / half;
+  const int i = int(g - run * half);
+  const long m0 = run * a.steps;
+  if (m0 >= a.M) return;
   const double f = scaled_frequency(a, i);
-  const long m1 = m0 + a.steps < a.M ? m0 + a.steps : a.M;
-  for (long m = m0; m < m1; ++m) {
-    double s, c;
-    sincos(double(a.P + m) * f, &s, &c);
-    *reinterpret_cast<float2*>(a.out + m * a.rot + 2 * i) =
+  const long m1 = min(m0 + a.steps, long(a.M)), mid = (m0 + m1) / 2;
+  float* out = a.out + 2 * i;
+  auto put = [&](long m, double c, double s) {
+    *reinterpret_cast<float2*>(out + m * a.rot) =
         make_float2(float(a.amplitude * c), float(a.amplitude * s));
+  };
+  double s0, c0;
+  sincos(double(a.P + mid) * f, &s0, &c0);
+  put(mid, c0, s0);
+  if (m1 - m0 == 1) return;
+  double ds, dc, cu = c0, su = s0, cd = c0, sd = s0;
+  sincos(f, &ds, &dc);
+  for (int k = 1; k <= mid - m0; ++k) {
+    double n = fma(cd, dc, sd * ds);
+    sd = fma(sd, dc, -(cd * ds));
+    cd = n;
+    put(mid - k, cd, sd);
+    if (mid + k < m1) {
+      n = fma(cu, dc, -(su * ds));
+      su = fma(su, dc, cu * ds);
+      cu = n;
+      put(mid + k, cu, su);
+    }
   }
 }
 
@@ -75,47 +102,87 @@ struct HeadArgs {
 
 enum { kToRows = 0, kToBf16Pages = 1, kToFp4Pages = 2 };
 
-// 8 elements of a head (fp32) to 8 e2m1 codes; the two lanes of a 16-element
-// block share its scale (header, frt_paged_kv_append); `group`: the lanes of
-// the head, all of which call it.
-__device__ __forceinline__ uint32_t quantise8(const float (&x)[8], float rk, uint32_t group,
-                                              uint8_t* scale) {
-  float y[8], a = 0.0f;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    y[j] = __fmul_rn(x[j], rk);
-    a = fmaxf(a, fabsf(y[j]));  // fmaxf drops NaN
+// Where a lane's two pieces of 8 elements lie in a head.  Lane l < rot/16
+// holds pieces l and rot/16 + l, which a rotation of halves pairs element by
+// element; the others share out what is not rotated.
+struct Pieces {
+  int turn, rest;  // rot / 16; lanes for the unrotated pieces
+  __device__ __forceinline__ int piece(int lane, int slot) const {
+    return lane < turn ? lane + slot * turn : 2 * turn + (lane - turn) + slot * rest;
   }
-  a = fmaxf(a, __shfl_xor_sync(group, a, 1));
+  // the lane and slot that hold a piece
+  __device__ __forceinline__ void find(int p, int* lane, int* slot) const {
+    const int i = p - 2 * turn;
+    *slot = i < 0 ? p >= turn : i >= rest;
+    *lane = i < 0 ? p - *slot * turn : turn + i - *slot * rest;
+  }
+};
+
+// bf16 bits (sign dropped) as the high word of the same number in fp64: the
+// exponent's bias moves by 896.  (A subnormal comes out at most 2^-126, whose
+// square counts for nothing; infinities and NaN come out 2^128 and above.)
+__device__ __forceinline__ double square_acc(uint32_t w, double acc) {
+  const double lo = __hiloint2double(int((w & 0x7FFFu) * 8192u + 0x38000000u), 0);
+  const double hi = __hiloint2double(int(((w & 0x7FFF0000u) >> 3) + 0x38000000u), 0);
+  return fma(hi, hi, fma(lo, lo, acc));
+}
+
+__device__ __forceinline__ float absmax8(const uint64_t (&y)[4]) {
+  float a = 0.0f;  // fmaxf drops NaN
+#pragma unroll
+  for (int j = 0; j < 4; ++j) a = absmax2(a, y[j]);
+  return a;
+}
+
+// 8 elements y of a block whose largest magnitude is `a` to e2m1 codes, and
+// the block's scale (header, frt_paged_kv_append).  y / scale is the
+// correctly rounded quotient, so that ties fall as the definition says:
+// q = y r with r the correctly rounded 1 / scale, corrected by its exact
+// remainder (Markstein 1990).
+__device__ __forceinline__ uint32_t quantise8(const uint64_t (&y)[4], float a, uint8_t* scale) {
   const __nv_fp8_storage_t s8 =
       __nv_cvt_float_to_fp8(__fdiv_rn(a, 6.0f), __NV_SATFINITE, __NV_E4M3);
   const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw(s8, __NV_E4M3)));
   *scale = s8;
   if (s == 0.0f) return 0;
+  const float r = __frcp_rn(s);
+  const uint64_t r2 = f2_pack(r, r), ns2 = f2_pack(-s, -s);
   uint32_t w = 0;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const float2 t = make_float2(__fdiv_rn(y[2 * j], s), __fdiv_rn(y[2 * j + 1], s));
-    w |= uint32_t(__nv_cvt_float2_to_fp4x2(t, __NV_E2M1, cudaRoundNearest)) << (8 * j);
+    uint64_t v = y[j];
+    if (a > 8192.0f)  // far past saturation; keeps infinities out of the remainder
+      v = f2_pack(fminf(fmaxf(f2_lo(v), -8192.0f), 8192.0f), fminf(fmaxf(f2_hi(v), -8192.0f), 8192.0f));
+    const uint64_t q = mul2(v, r2);
+    const uint64_t t = fma2(fma2(q, ns2, v), r2, q);
+    w |= uint32_t(__nv_cvt_float2_to_fp4x2(make_float2(f2_lo(t), f2_hi(t)), __NV_E2M1,
+                                           cudaRoundNearest)) << (8 * j);
   }
   return w;
 }
 
-// LANES lanes hold a head, 8 elements each (lanes past hd / 8 idle); a group
-// of LANES lanes takes U consecutive heads of one row.  Everything the group
-// needs is requested before the first use.
+// LANES lanes hold a head, 16 elements each in two pieces (lanes past hd / 16
+// idle); a group of LANES lanes takes U consecutive heads of one row, all
+// requested before the first use.  Bound by bytes: about 190 instructions for
+// the 512 elements of a warp, normed, rotated and stored.
 template <int LANES, int U, int TO>
 __global__ void __launch_bounds__(256) head_kernel(HeadArgs a) {
   const int lane = int(threadIdx.x) % LANES;
   // the group's lanes of the warp: other groups may be at other kinds of heads
   const uint32_t group = (0xffffffffu >> (32 - LANES)) << (threadIdx.x % 32 / LANES * LANES);
   const int parts = (a.heads + U - 1) / U;
-  const long unit = (long(blockIdx.x) * blockDim.x + threadIdx.x) / LANES;
-  const long row = unit / parts;
-  const int h0 = a.first + int(unit - row * parts) * U;
+  const uint32_t unit = uint32_t(blockIdx.x) * (256 / LANES) + threadIdx.x / LANES;
+  const uint32_t row32 = unit / uint32_t(parts);
+  const long row = row32;
+  const int h0 = a.first + int(unit - row32 * uint32_t(parts)) * U;
   const int h_end = a.first + a.heads;
   const bool live = row < a.rows;       // the whole group's: it shares a row
-  const bool mine = live && lane * 8 < a.hd;
+  Pieces at;
+  at.turn = a.rot / 16;
+  at.rest = (a.hd / 8 - 2 * at.turn + 1) / 2;
+  const int p0 = at.piece(lane, 0), p1 = at.piece(lane, 1);
+  const bool has0 = live && p0 * 8 < a.hd && lane < at.turn + at.rest;
+  const bool has1 = has0 && p1 * 8 < a.hd;
   pdl_trigger();
   pdl_wait();
 
@@ -124,106 +191,149 @@ __global__ void __launch_bounds__(256) head_kernel(HeadArgs a) {
   if constexpr (TO != kToRows) {
     if (live) slot = a.slots[row];
   }
-  uint4 xv[U];
+  uint4 x0[U], x1[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u)
-    if (mine && h0 + u < h_end)
-      xv[u] = *reinterpret_cast<const uint4*>(a.qkv + row * a.ld_qkv + long(h0 + u) * a.hd + lane * 8);
-    else
-      xv[u] = make_uint4(0, 0, 0, 0);
+  for (int u = 0; u < U; ++u) {
+    const uint16_t* src = a.qkv + row * a.ld_qkv + long(h0 + u) * a.hd;
+    const bool on = h0 + u < h_end;
+    x0[u] = x1[u] = make_uint4(0, 0, 0, 0);
+    if (has0 && on) x0[u] = *reinterpret_cast<const uint4*>(src + p0 * 8);
+    if (has1 && on) x1[u] = *reinterpret_cast<const uint4*>(src + p1 * 8);
+  }
 
   const bool bad_pos = a.rot > 0 && (pos < 0 || pos >= a.n_pos);
   bool bad_slot = false;
   if constexpr (TO != kToRows) bad_slot = slot >= a.pool.slots();
   if (live && (bad_pos || bad_slot) && lane == 0) atomicExch(a.status, FRT_ERANGE);
 
-  // this lane's (cos, sin): pairs 4*lane.. (adjacent) or 8*lane.. modulo rot/2 (halves)
-  const bool rotates = mine && lane * 8 < a.rot && !bad_pos;
-  const int half_lanes = a.rot / 16;
-  const bool second = lane >= half_lanes;
+  // this lane's cos and sin: of the 8 pairs (piece 0, piece 1), or of the 4
+  // adjacent pairs of each piece
+  const bool half = a.layout == FRT_ROPE_HALF;
+  const bool rotates = live && lane < at.turn && !bad_pos;
   float cs[16];
   if (rotates) {
     const float* t = a.rope + pos * a.rot;
-    const int n4 = a.layout == FRT_ROPE_HALF ? 4 : 2;
-    t += a.layout == FRT_ROPE_HALF ? (second ? lane - half_lanes : lane) * 16 : lane * 8;
+    const int o0 = half ? lane * 16 : p0 * 8, o1 = half ? lane * 16 + 8 : p1 * 8;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (j < n4) {
-        const float4 v = *reinterpret_cast<const float4*>(t + 4 * j);
-        cs[4 * j] = v.x; cs[4 * j + 1] = v.y; cs[4 * j + 2] = v.z; cs[4 * j + 3] = v.w;
-      }
+    for (int j = 0; j < 4; ++j) {
+      const float4 v = *reinterpret_cast<const float4*>(t + (j < 2 ? o0 : o1) + j % 2 * 4);
+      cs[4 * j] = v.x; cs[4 * j + 1] = v.y; cs[4 * j + 2] = v.z; cs[4 * j + 3] = v.w;
+    }
   }
-  const int partner = second ? lane - half_lanes : lane + half_lanes;
 
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int h = h0 + u;
-    const bool on = h < h_end;
+    if (h >= h_end) break;                // the whole group's
     const bool is_q = h < a.hq, is_v = h >= a.hq + a.hkv;
-    float x[8];
-    unpack8(xv[u], x);
-    const uint16_t* w = is_v ? nullptr : is_q ? a.q_norm : a.k_norm;
-    float r = 1.0f;
-    if (w) {  // uniform over the group: it depends on h alone
-      // squares of bf16 are exact in fp32; the sum is carried in fp64, so
-      // that a key next to a 4-bit border does not depend on its order
-      double s = 0.0;
+    uint4 o0 = x0[u], o1 = x1[u];
+    const uint16_t* w = is_q ? a.q_norm : a.k_norm;
+    const bool normed = !is_v && w;
+    if (normed || (!is_v && a.rot > 0)) {
+      uint64_t y[2][4];
+      unpack8_f2(x0[u], y[0]);
+      unpack8_f2(x1[u], y[1]);
+      if (normed) {
+        uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
+        if (has0) w0 = *reinterpret_cast<const uint4*>(w + p0 * 8);
+        if (has1) w1 = *reinterpret_cast<const uint4*>(w + p1 * 8);
+        // the sum of squares in fp64: a key next to a 4-bit border must not
+        // depend on the order of its summands
+        double s = 0.0, s1 = 0.0;
+        s = square_acc(x0[u].x, s); s1 = square_acc(x0[u].y, s1);
+        s = square_acc(x0[u].z, s); s1 = square_acc(x0[u].w, s1);
+        s = square_acc(x1[u].x, s); s1 = square_acc(x1[u].y, s1);
+        s = square_acc(x1[u].z, s); s1 = square_acc(x1[u].w, s1);
+        s += s1;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s += double(x[j] * x[j]);
+        for (int o = LANES / 2; o > 0; o >>= 1) s += __shfl_xor_sync(group, s, o, LANES);
+        const float m = __fadd_rn(float(s * a.inv_hd), a.eps);
+        float r = __frcp_rn(__fsqrt_rn(m));
+        if (isinf(m)) {  // NaN among the elements makes the head NaN
+          bool nan = false;
 #pragma unroll
-      for (int o = LANES / 2; o > 0; o >>= 1)
-        s += __shfl_xor_sync(group, s, o, LANES);
-      const float m = __fadd_rn(float(s * a.inv_hd), a.eps);
-      r = __frcp_rn(__fsqrt_rn(m));
-      float wv[8];
-      if (mine) {
-        unpack8(*reinterpret_cast<const uint4*>(w + lane * 8), wv);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = __fmul_rn(__fmul_rn(x[j], r), wv[j]);
-      }
-    }
-    if (!is_v && a.rot > 0) {
-      if (a.layout == FRT_ROPE_HALF) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float o = __shfl_sync(group, x[j], partner, LANES);
-          if (rotates)
-            x[j] = second ? __fadd_rn(__fmul_rn(o, cs[2 * j + 1]), __fmul_rn(x[j], cs[2 * j]))
-                          : __fsub_rn(__fmul_rn(x[j], cs[2 * j]), __fmul_rn(o, cs[2 * j + 1]));
+          for (int j = 0; j < 4; ++j)
+            nan |= isnan(f2_lo(y[0][j])) | isnan(f2_hi(y[0][j])) | isnan(f2_lo(y[1][j])) | isnan(f2_hi(y[1][j]));
+          if (__any_sync(group, nan)) r = NAN;
         }
-      } else if (rotates) {
+        uint64_t wv[2][4];
+        unpack8_f2(w0, wv[0]);
+        unpack8_f2(w1, wv[1]);
+        const uint64_t r2 = f2_pack(r, r);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float x0 = x[2 * j], x1 = x[2 * j + 1], c = cs[2 * j], s = cs[2 * j + 1];
-          x[2 * j] = __fsub_rn(__fmul_rn(x0, c), __fmul_rn(x1, s));
-          x[2 * j + 1] = __fadd_rn(__fmul_rn(x0, s), __fmul_rn(x1, c));
+          y[0][j] = mul2(mul2(y[0][j], r2), wv[0][j]);
+          y[1][j] = mul2(mul2(y[1][j], r2), wv[1][j]);
         }
       }
+      if (rotates) {
+        if (half) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint64_t c = f2_pack(cs[4 * j], cs[4 * j + 2]), s = f2_pack(cs[4 * j + 1], cs[4 * j + 3]);
+            const uint64_t u0 = y[0][j], u1 = y[1][j];
+            y[0][j] = sub2(mul2(u0, c), mul2(u1, s));
+            y[1][j] = add2(mul2(u0, s), mul2(u1, c));
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            uint64_t& v = y[j / 4][j % 4];
+            const float e0 = f2_lo(v), e1 = f2_hi(v), c = cs[2 * j], s = cs[2 * j + 1];
+            v = f2_pack(__fsub_rn(__fmul_rn(e0, c), __fmul_rn(e1, s)),
+                        __fadd_rn(__fmul_rn(e0, s), __fmul_rn(e1, c)));
+          }
+        }
+      }
+      o0 = pack8_bf16_f2(y[0]);
+      o1 = pack8_bf16_f2(y[1]);
     }
-    const uint4 o = pack8_bf16(x);
-    const bool write = mine && on && !bad_pos;
-    if (is_q) {
-      if (write) *reinterpret_cast<uint4*>(a.q_out + row * a.ld_q + long(h) * a.hd + lane * 8) = o;
-    } else if constexpr (TO == kToRows) {
-      if (write)
-        *reinterpret_cast<uint4*>(a.k_out + row * a.ld_k + long(h - a.hq) * a.hd + lane * 8) = o;
+    if (TO == kToRows || is_q) {
+      uint16_t* dst = is_q ? a.q_out + row * a.ld_q + long(h) * a.hd
+                           : a.k_out + row * a.ld_k + long(h - a.hq) * a.hd;
+      if (has0 && !bad_pos) *reinterpret_cast<uint4*>(dst + p0 * 8) = o0;
+      if (has1 && !bad_pos) *reinterpret_cast<uint4*>(dst + p1 * 8) = o1;
     } else {
       const int kvh = is_v ? h - a.hq - a.hkv : h - a.hq;
-      const bool cached = write && slot >= 0 && !bad_slot;
-      uint8_t* rec = cached ? a.pool.record(slot, kvh) : nullptr;
-      const int at = cached ? a.pool.row(slot) : 0;
+      const bool cached = slot >= 0 && !bad_slot && !bad_pos;   // the group's
+      if (!cached) continue;
+      uint8_t* rec = a.pool.record(slot, kvh);
+      const long row_in = a.pool.row(slot);
       if constexpr (TO == kToBf16Pages) {
-        if (cached)
-          *reinterpret_cast<uint4*>(rec + (long(is_v ? a.pool.page_size : 0) + at) * a.hd * 2 + lane * 16) = o;
+        uint8_t* dst = rec + ((is_v ? a.pool.page_size : 0) + row_in) * a.hd * 2;
+        if (has0) *reinterpret_cast<uint4*>(dst + p0 * 16) = o0;
+        if (has1) *reinterpret_cast<uint4*>(dst + p1 * 16) = o1;
       } else {
-        unpack8(o, x);  // what is cached is the bf16 key
-        uint8_t s8;
-        const uint32_t codes = quantise8(x, __frcp_rn(*(is_v ? a.v_scale : a.k_scale)), group, &s8);
-        if (cached) {
-          rec += is_v ? a.pool.record_bytes / 2 : 0;
-          *reinterpret_cast<uint32_t*>(rec + long(at) * (a.hd / 2) + lane * 4) = codes;
-          if ((lane & 1) == 0)
-            rec[a.pool.page_size * (a.hd / 2) + long(at) * (a.hd / 16) + lane / 2] = s8;
+        const float rk = __frcp_rn(*(is_v ? a.v_scale : a.k_scale));
+        const uint64_t rk2 = f2_pack(rk, rk);
+        uint64_t y[2][4];
+        unpack8_f2(o0, y[0]);  // what is cached is the bf16 key
+        unpack8_f2(o1, y[1]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          y[0][j] = mul2(y[0][j], rk2);
+          y[1][j] = mul2(y[1][j], rk2);
+        }
+        // a block of 16 is two neighbouring pieces: the other one's largest
+        float big[2] = {absmax8(y[0]), absmax8(y[1])}, all[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          int l, sl;
+          at.find((i ? p1 : p0) ^ 1, &l, &sl);
+          const float b0 = __shfl_sync(group, big[0], l, LANES), b1 = __shfl_sync(group, big[1], l, LANES);
+          all[i] = fmaxf(big[i], sl ? b1 : b0);
+        }
+        rec += is_v ? a.pool.record_bytes / 2 : 0;
+        uint8_t* scales = rec + long(a.pool.page_size) * (a.hd / 2) + row_in * (a.hd / 16);
+        rec += row_in * (a.hd / 2);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int p = i ? p1 : p0;
+          if (!(i ? has1 : has0)) continue;
+          uint8_t s8;
+          const uint32_t codes = quantise8(y[i], all[i], &s8);
+          *reinterpret_cast<uint32_t*>(rec + p * 4) = codes;
+          if ((p & 1) == 0) scales[p / 2] = s8;
         }
       }
     }
@@ -234,7 +344,7 @@ template <int LANES, int U>
 int launch_heads(int to, const HeadArgs& a, cudaStream_t s) {
   const long units = long(a.rows) * ((a.heads + U - 1) / U);
   const long blocks = (units * LANES + 255) / 256;
-  FRT_REQUIRE(blocks <= 0x7fffffffL, FRT_ESHAPE, "rows * heads is too large");
+  FRT_REQUIRE(units <= 0x7fffff00L, FRT_ESHAPE, "rows * heads is too large");
   const dim3 grid{unsigned(blocks)}, block{256};
   switch (to) {
     case kToRows: return launch_pdl("frt_qk_norm_rope", head_kernel<LANES, U, kToRows>, grid, block, 0, s, a);
@@ -246,11 +356,11 @@ int launch_heads(int to, const HeadArgs& a, cudaStream_t s) {
 int launch_heads(int to, const HeadArgs& a, cudaStream_t s) {
   // One head a group while the heads do not fill the GPU (latency), four
   // once they do (the table row and the index arithmetic are shared).
-  const int lanes = a.hd <= 64 ? 8 : a.hd <= 128 ? 16 : 32;
+  const int lanes = a.hd <= 64 ? 4 : a.hd <= 128 ? 8 : 16;
   const bool few = long(a.rows) * a.heads * lanes <= num_sms() * 2048L;
+  if (lanes == 4) return few ? launch_heads<4, 1>(to, a, s) : launch_heads<4, 4>(to, a, s);
   if (lanes == 8) return few ? launch_heads<8, 1>(to, a, s) : launch_heads<8, 4>(to, a, s);
-  if (lanes == 16) return few ? launch_heads<16, 1>(to, a, s) : launch_heads<16, 4>(to, a, s);
-  return few ? launch_heads<32, 1>(to, a, s) : launch_heads<32, 4>(to, a, s);
+  return few ? launch_heads<16, 1>(to, a, s) : launch_heads<16, 4>(to, a, s);
 }
 
 // ------------------------------------------------------------------ read --
@@ -265,18 +375,20 @@ struct ReadArgs {
   int* status;
 };
 
-// One thread per 8 elements of a cached head.
+// One thread per 16 elements of a cached head (8 in bf16 pages): a block's
+// codes and scale.  Bound by bytes.
 __global__ void __launch_bounds__(256) read_kernel(ReadArgs a) {
-  const int hd8 = a.hd / 8;
-  const long g = blockIdx.x * 256L + threadIdx.x;
+  const uint32_t pieces = uint32_t(a.hd) / (a.fp4 ? 16 : 8);
+  const uint32_t per_row = 2u * a.hkv * pieces;
+  const uint32_t g = blockIdx.x * 256u + threadIdx.x;
   pdl_trigger();
   pdl_wait();
-  const long row = g / (2L * a.hkv * hd8);
-  if (row >= a.rows) return;
-  const int c = int(g - row * (2L * a.hkv * hd8));
-  const int h2 = c / hd8, p = c - h2 * hd8;  // h2: the k heads, then the v heads
-  const bool is_v = h2 >= a.hkv;
-  const int h = is_v ? h2 - a.hkv : h2;
+  const uint32_t row = g / per_row;
+  if (row >= uint32_t(a.rows)) return;
+  const uint32_t c = g - row * per_row;
+  const uint32_t h2 = c / pieces, p = c - h2 * pieces;  // h2: the k heads, then the v heads
+  const bool is_v = h2 >= uint32_t(a.hkv);
+  const int h = int(is_v ? h2 - a.hkv : h2);
   uint16_t* out = is_v ? a.v_out : a.k_out;
   if (!out) return;
   const long slot = a.slots[row];
@@ -286,26 +398,29 @@ __global__ void __launch_bounds__(256) read_kernel(ReadArgs a) {
     return;
   }
   const uint8_t* rec = a.pool.record(slot, h);
-  const int at = a.pool.row(slot);
-  uint4 o;
-  if (a.fp4) {
-    rec += is_v ? a.pool.record_bytes / 2 : 0;
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(rec + long(at) * (a.hd / 2) + p * 4);
-    const __nv_fp8_storage_t s8 = rec[a.pool.page_size * (a.hd / 2) + long(at) * (a.hd / 16) + p / 2];
-    const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw(s8, __NV_E4M3)));
-    const float k = *(is_v ? a.v_scale : a.k_scale);
+  const long at = a.pool.row(slot);
+  out += row * (is_v ? a.ld_v : a.ld_k) + long(h) * a.hd;
+  if (!a.fp4) {
+    reinterpret_cast<uint4*>(out)[p] =
+        *reinterpret_cast<const uint4*>(rec + ((is_v ? a.pool.page_size : 0) + at) * a.hd * 2 + p * 16);
+    return;
+  }
+  rec += is_v ? a.pool.record_bytes / 2 : 0;
+  const uint2 w = *reinterpret_cast<const uint2*>(rec + at * (a.hd / 2) + p * 8);
+  const __nv_fp8_storage_t s8 = rec[long(a.pool.page_size) * (a.hd / 2) + at * (a.hd / 16) + p];
+  const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw(s8, __NV_E4M3)));
+  const float k = *(is_v ? a.v_scale : a.k_scale);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
     float x[8];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const __half2 v(__nv_cvt_fp4x2_to_halfraw2(__nv_fp4x2_storage_t(w >> (8 * j)), __NV_E2M1));
+      const __half2 v(__nv_cvt_fp4x2_to_halfraw2(__nv_fp4x2_storage_t((i ? w.y : w.x) >> (8 * j)), __NV_E2M1));
       x[2 * j] = __fmul_rn(__fmul_rn(__low2float(v), s), k);
       x[2 * j + 1] = __fmul_rn(__fmul_rn(__high2float(v), s), k);
     }
-    o = pack8_bf16(x);
-  } else {
-    o = *reinterpret_cast<const uint4*>(rec + (long(is_v ? a.pool.page_size : 0) + at) * a.hd * 2 + p * 16);
+    reinterpret_cast<uint4*>(out)[2 * p + i] = pack8_bf16(x);
   }
-  *reinterpret_cast<uint4*>(out + row * (is_v ? a.ld_v : a.ld_k) + long(h) * a.hd + p * 8) = o;
 }
 
 // ---------------------------------------------------------------- checks --
@@ -410,7 +525,16 @@ extern "C" int frt_build_rope_table_scaled(int M, int rot, long P, double theta,
   FRT_REQUIRE(rope_out, FRT_EINVAL, "rope_out is required");
   FRT_REQUIRE(frt::aligned(rope_out, 8), FRT_EALIGN, "rope_out must be 8-byte aligned");
   if (M == 0) return FRT_OK;
-  frt::TableArgs a{M, rot, scaling, 1, P, theta, factor, orig_len, low_turns, high_turns, amplitude, rope_out};
+  frt::TableArgs a{};
+  a.M = M; a.rot = rot; a.scaling = scaling; a.P = P; a.factor = factor; a.orig_len = orig_len;
+  a.low = low_turns; a.high = high_turns; a.amplitude = amplitude; a.out = rope_out;
+  long double base = log2l((long double)theta);
+  if (scaling == FRT_ROPE_SCALE_BASE) base += log2l((long double)factor) * rot / (rot - 2);
+  a.log2_base = double(base);
+  a.log2_base_lo = double(base - a.log2_base);
+  // runs as long as the GPU stays full, 32 at most
+  const long per_thread = long(M) * (rot / 2) / (frt::num_sms() * 1024L);
+  a.steps = per_thread < 1 ? 1 : per_thread > 32 ? 32 : int(per_thread);
   const long threads = (long(M) + a.steps - 1) / a.steps * (rot / 2);
   const long blocks = (threads + 255) / 256;
   FRT_REQUIRE(blocks <= 0x7fffffffL, FRT_ESHAPE, "M * rot is too large");
@@ -480,8 +604,9 @@ extern "C" int frt_paged_kv_read(const frt_qk_rope_desc* d, void* stream) {
                   d->k_scale, d->v_scale, d->k_out, d->ld_k, d->v_out, d->ld_v,
                   frt::device_status_ptr()};
   FRT_REQUIRE(a.status, FRT_ECUDA, "device status word unavailable");
-  const long blocks = (2L * d->rows * d->hkv * (d->hd / 8) + 255) / 256;
-  FRT_REQUIRE(blocks <= 0x7fffffffL, FRT_ESHAPE, "rows * heads is too large");
+  const long threads = 2L * d->rows * d->hkv * (d->hd / (a.fp4 ? 16 : 8));
+  FRT_REQUIRE(threads <= 0xffffff00L, FRT_ESHAPE, "rows * heads is too large");
+  const long blocks = (threads + 255) / 256;
   return frt::launch_pdl("frt_paged_kv_read", frt::read_kernel, dim3(unsigned(blocks)), dim3(256),
                          0, static_cast<cudaStream_t>(stream), a);
 }
