@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(256) rope_table_scaled_kernel(TableArgs a) {
 
 struct HeadArgs {
   int rows, hq, hkv, hd, rot, layout;
-  int first, heads;     // heads [first, first + heads) of a row are done
+  int q_units;          // groups of U q heads in a row
   float eps;
   double inv_hd;
   const uint16_t* qkv; long ld_qkv;
@@ -118,15 +118,6 @@ struct Pieces {
   }
 };
 
-// bf16 bits (sign dropped) as the high word of the same number in fp64: the
-// exponent's bias moves by 896.  (A subnormal comes out at most 2^-126, whose
-// square counts for nothing; infinities and NaN come out 2^128 and above.)
-__device__ __forceinline__ double square_acc(uint32_t w, double acc) {
-  const double lo = __hiloint2double(int((w & 0x7FFFu) * 8192u + 0x38000000u), 0);
-  const double hi = __hiloint2double(int(((w & 0x7FFF0000u) >> 3) + 0x38000000u), 0);
-  return fma(hi, hi, fma(lo, lo, acc));
-}
-
 __device__ __forceinline__ float absmax8(const uint64_t (&y)[4]) {
   float a = 0.0f;  // fmaxf drops NaN
 #pragma unroll
@@ -134,49 +125,61 @@ __device__ __forceinline__ float absmax8(const uint64_t (&y)[4]) {
   return a;
 }
 
-// 8 elements y of a block whose largest magnitude is `a` to e2m1 codes, and
-// the block's scale (header, frt_paged_kv_append).  y / scale is the
-// correctly rounded quotient, so that ties fall as the definition says:
-// q = y r with r the correctly rounded 1 / scale, corrected by its exact
-// remainder (Markstein 1990).
-__device__ __forceinline__ uint32_t quantise8(const uint64_t (&y)[4], float a, uint8_t* scale) {
-  const __nv_fp8_storage_t s8 =
-      __nv_cvt_float_to_fp8(__fdiv_rn(a, 6.0f), __NV_SATFINITE, __NV_E4M3);
+// The scale of a block whose largest magnitude is `a` (header,
+// frt_paged_kv_append).  a / 6 and y / scale below are correctly rounded
+// quotients, so that ties fall as the definition says: q = x r with r the
+// correctly rounded reciprocal, corrected by its exact remainder (Markstein
+// 1990).  a is held to 8192, far past the largest scale's 2688.
+__device__ __forceinline__ uint8_t block_scale(float a) {
+  a = fminf(a, 8192.0f);
+  constexpr float kSixth = 1.0f / 6.0f;
+  const float q = __fmul_rn(a, kSixth);
+  const float t = __fmaf_rn(__fmaf_rn(q, -6.0f, a), kSixth, q);
+  return __nv_cvt_float_to_fp8(t, __NV_SATFINITE, __NV_E4M3);
+}
+
+// 8 elements y of a block with that scale to e2m1 codes.
+__device__ __forceinline__ uint32_t quantise8(const uint64_t (&y)[4], uint8_t s8) {
   const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw(s8, __NV_E4M3)));
-  *scale = s8;
-  if (s == 0.0f) return 0;
-  const float r = __frcp_rn(s);
+  const float r = s == 0.0f ? 0.0f : __frcp_rn(s);   // scale 0: codes 0
   const uint64_t r2 = f2_pack(r, r), ns2 = f2_pack(-s, -s);
   uint32_t w = 0;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    uint64_t v = y[j];
-    if (a > 8192.0f)  // far past saturation; keeps infinities out of the remainder
-      v = f2_pack(fminf(fmaxf(f2_lo(v), -8192.0f), 8192.0f), fminf(fmaxf(f2_hi(v), -8192.0f), 8192.0f));
-    const uint64_t q = mul2(v, r2);
-    const uint64_t t = fma2(fma2(q, ns2, v), r2, q);
+    const uint64_t q = mul2(y[j], r2);
+    const uint64_t t = fma2(fma2(q, ns2, y[j]), r2, q);
     w |= uint32_t(__nv_cvt_float2_to_fp4x2(make_float2(f2_lo(t), f2_hi(t)), __NV_E2M1,
                                            cudaRoundNearest)) << (8 * j);
   }
-  return w;
+  return s == 0.0f ? 0 : w;
 }
 
 // LANES lanes hold a head, 16 elements each in two pieces (lanes past hd / 16
-// idle); a group of LANES lanes takes U consecutive heads of one row, all
-// requested before the first use.  Bound by bytes: about 190 instructions for
-// the 512 elements of a warp, normed, rotated and stored.
+// idle); a group of LANES lanes takes U consecutive heads of one kind (q, k
+// or v) of one row, one after another, the next one's elements under way.
+// Bound by bytes: 8192 rows of 24 + 24 heads of 128, normed and rotated, run
+// at 4.6 TB/s (44 us); 24 warps an SM (80 registers) measured better than 16
+// with more registers (54 us) and than 32 with spills (63 us), one loop over
+// the heads better than U heads in registers at once (58 us).
 template <int LANES, int U, int TO>
-__global__ void __launch_bounds__(256) head_kernel(HeadArgs a) {
+__global__ void __launch_bounds__(256, U == 1 ? 2 : 3) head_kernel(HeadArgs a) {
   const int lane = int(threadIdx.x) % LANES;
   // the group's lanes of the warp: other groups may be at other kinds of heads
   const uint32_t group = (0xffffffffu >> (32 - LANES)) << (threadIdx.x % 32 / LANES * LANES);
-  const int parts = (a.heads + U - 1) / U;
-  const uint32_t unit = uint32_t(blockIdx.x) * (256 / LANES) + threadIdx.x / LANES;
-  const uint32_t row32 = unit / uint32_t(parts);
+  // all rows' q heads, then all k heads, then all v heads: a warp's groups
+  // are at one kind, and so on one path
+  uint32_t unit = uint32_t(blockIdx.x) * (256 / LANES) + threadIdx.x / LANES;
+  const uint32_t kv_units = (uint32_t(a.hkv) + U - 1) / U;
+  const uint32_t n_q = uint32_t(a.rows) * a.q_units, n_k = uint32_t(a.rows) * kv_units;
+  const bool is_q = unit < n_q, is_v = unit >= n_q + n_k;
+  unit -= is_q ? 0 : is_v ? n_q + n_k : n_q;
+  const uint32_t per_row = is_q ? a.q_units : kv_units;
+  const uint32_t row32 = unit / per_row;
   const long row = row32;
-  const int h0 = a.first + int(unit - row32 * uint32_t(parts)) * U;
-  const int h_end = a.first + a.heads;
-  const bool live = row < a.rows;       // the whole group's: it shares a row
+  const int j0 = int(unit - row32 * per_row) * U;  // of the kind's heads
+  const int jn = min(U, (is_q ? a.hq : a.hkv) - j0);
+  const int h0 = j0 + (is_q ? 0 : a.hq) + (is_v ? a.hkv : 0);
+  const bool live = row < a.rows && (TO != kToRows || !is_v);  // the whole group's
   Pieces at;
   at.turn = a.rot / 16;
   at.rest = (a.hd / 8 - 2 * at.turn + 1) / 2;
@@ -191,15 +194,19 @@ __global__ void __launch_bounds__(256) head_kernel(HeadArgs a) {
   if constexpr (TO != kToRows) {
     if (live) slot = a.slots[row];
   }
-  uint4 x0[U], x1[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const uint16_t* src = a.qkv + row * a.ld_qkv + long(h0 + u) * a.hd;
-    const bool on = h0 + u < h_end;
-    x0[u] = x1[u] = make_uint4(0, 0, 0, 0);
-    if (has0 && on) x0[u] = *reinterpret_cast<const uint4*>(src + p0 * 8);
-    if (has1 && on) x1[u] = *reinterpret_cast<const uint4*>(src + p1 * 8);
+  const uint16_t* src = a.qkv + row * a.ld_qkv + long(h0) * a.hd;
+  uint4 n0 = make_uint4(0, 0, 0, 0), n1 = n0;   // the next head's pieces
+  if (has0) n0 = *reinterpret_cast<const uint4*>(src + p0 * 8);
+  if (has1) n1 = *reinterpret_cast<const uint4*>(src + p1 * 8);
+
+  const uint16_t* w = is_v ? nullptr : is_q ? a.q_norm : a.k_norm;
+  uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
+  if (w) {
+    if (has0) w0 = *reinterpret_cast<const uint4*>(w + p0 * 8);
+    if (has1) w1 = *reinterpret_cast<const uint4*>(w + p1 * 8);
   }
+  float static_scale = 1.0f;
+  if constexpr (TO == kToFp4Pages) static_scale = *(is_v ? a.v_scale : a.k_scale);
 
   const bool bad_pos = a.rot > 0 && (pos < 0 || pos >= a.n_pos);
   bool bad_slot = false;
@@ -209,7 +216,7 @@ __global__ void __launch_bounds__(256) head_kernel(HeadArgs a) {
   // this lane's cos and sin: of the 8 pairs (piece 0, piece 1), or of the 4
   // adjacent pairs of each piece
   const bool half = a.layout == FRT_ROPE_HALF;
-  const bool rotates = live && lane < at.turn && !bad_pos;
+  const bool rotates = live && lane < at.turn && !bad_pos && !is_v;
   float cs[16];
   if (rotates) {
     const float* t = a.rope + pos * a.rot;
@@ -221,128 +228,147 @@ __global__ void __launch_bounds__(256) head_kernel(HeadArgs a) {
     }
   }
 
+  // the next head's pieces, and on to the one after it
+  auto advance = [&](int u, uint4& o0, uint4& o1) {
+    o0 = n0;
+    o1 = n1;
+    if (u + 1 < jn) {
+      src += a.hd;
+      if (has0) n0 = *reinterpret_cast<const uint4*>(src + p0 * 8);
+      if (has1) n1 = *reinterpret_cast<const uint4*>(src + p1 * 8);
+    }
+  };
+  // the norm and the rotation of one head, rounded to bf16
+  auto norm_rotate = [&](uint4& o0, uint4& o1) {
+    if (!w && a.rot == 0) return;
+    uint64_t y[2][4];
+    unpack8_f2(o0, y[0]);
+    unpack8_f2(o1, y[1]);
+    if (w) {
+      // the sum of squares in fp64: a key next to a 4-bit border must not
+      // depend on the order of its summands
+      double s = 0.0, s1 = 0.0;
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int h = h0 + u;
-    if (h >= h_end) break;                // the whole group's
-    const bool is_q = h < a.hq, is_v = h >= a.hq + a.hkv;
-    uint4 o0 = x0[u], o1 = x1[u];
-    const uint16_t* w = is_q ? a.q_norm : a.k_norm;
-    const bool normed = !is_v && w;
-    if (normed || (!is_v && a.rot > 0)) {
-      uint64_t y[2][4];
-      unpack8_f2(x0[u], y[0]);
-      unpack8_f2(x1[u], y[1]);
-      if (normed) {
-        uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
-        if (has0) w0 = *reinterpret_cast<const uint4*>(w + p0 * 8);
-        if (has1) w1 = *reinterpret_cast<const uint4*>(w + p1 * 8);
-        // the sum of squares in fp64: a key next to a 4-bit border must not
-        // depend on the order of its summands
-        double s = 0.0, s1 = 0.0;
-        s = square_acc(x0[u].x, s); s1 = square_acc(x0[u].y, s1);
-        s = square_acc(x0[u].z, s); s1 = square_acc(x0[u].w, s1);
-        s = square_acc(x1[u].x, s); s1 = square_acc(x1[u].y, s1);
-        s = square_acc(x1[u].z, s); s1 = square_acc(x1[u].w, s1);
-        s += s1;
-#pragma unroll
-        for (int o = LANES / 2; o > 0; o >>= 1) s += __shfl_xor_sync(group, s, o, LANES);
-        const float m = __fadd_rn(float(s * a.inv_hd), a.eps);
-        float r = __frcp_rn(__fsqrt_rn(m));
-        if (isinf(m)) {  // NaN among the elements makes the head NaN
-          bool nan = false;
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            nan |= isnan(f2_lo(y[0][j])) | isnan(f2_hi(y[0][j])) | isnan(f2_lo(y[1][j])) | isnan(f2_hi(y[1][j]));
-          if (__any_sync(group, nan)) r = NAN;
-        }
-        uint64_t wv[2][4];
-        unpack8_f2(w0, wv[0]);
-        unpack8_f2(w1, wv[1]);
-        const uint64_t r2 = f2_pack(r, r);
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          y[0][j] = mul2(mul2(y[0][j], r2), wv[0][j]);
-          y[1][j] = mul2(mul2(y[1][j], r2), wv[1][j]);
+          const double lo = f2_lo(y[i][j]), hi = f2_hi(y[i][j]);
+          s = fma(lo, lo, s);
+          s1 = fma(hi, hi, s1);
         }
-      }
-      if (rotates) {
-        if (half) {
+      s += s1;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint64_t c = f2_pack(cs[4 * j], cs[4 * j + 2]), s = f2_pack(cs[4 * j + 1], cs[4 * j + 3]);
-            const uint64_t u0 = y[0][j], u1 = y[1][j];
-            y[0][j] = sub2(mul2(u0, c), mul2(u1, s));
-            y[1][j] = add2(mul2(u0, s), mul2(u1, c));
-          }
-        } else {
+      for (int o = LANES / 2; o > 0; o >>= 1) s += __shfl_xor_sync(group, s, o, LANES);
+      const float m = __fadd_rn(float(s * a.inv_hd), a.eps);
+      const float r = __frcp_rn(__fsqrt_rn(m));
+      uint64_t wv[2][4];
+      unpack8_f2(w0, wv[0]);
+      unpack8_f2(w1, wv[1]);
+      const uint64_t r2 = f2_pack(r, r);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            uint64_t& v = y[j / 4][j % 4];
-            const float e0 = f2_lo(v), e1 = f2_hi(v), c = cs[2 * j], s = cs[2 * j + 1];
-            v = f2_pack(__fsub_rn(__fmul_rn(e0, c), __fmul_rn(e1, s)),
-                        __fadd_rn(__fmul_rn(e0, s), __fmul_rn(e1, c)));
-          }
-        }
+      for (int j = 0; j < 4; ++j) {
+        y[0][j] = mul2(mul2(y[0][j], r2), wv[0][j]);
+        y[1][j] = mul2(mul2(y[1][j], r2), wv[1][j]);
       }
-      o0 = pack8_bf16_f2(y[0]);
-      o1 = pack8_bf16_f2(y[1]);
     }
-    if (TO == kToRows || is_q) {
-      uint16_t* dst = is_q ? a.q_out + row * a.ld_q + long(h) * a.hd
-                           : a.k_out + row * a.ld_k + long(h - a.hq) * a.hd;
+    if (rotates) {
+      if (half) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint64_t c = f2_pack(cs[4 * j], cs[4 * j + 2]), s = f2_pack(cs[4 * j + 1], cs[4 * j + 3]);
+          const uint64_t u0 = y[0][j], u1 = y[1][j];
+          y[0][j] = sub2(mul2(u0, c), mul2(u1, s));
+          y[1][j] = add2(mul2(u0, s), mul2(u1, c));
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          uint64_t& v = y[j / 4][j % 4];
+          const float e0 = f2_lo(v), e1 = f2_hi(v), c = cs[2 * j], s = cs[2 * j + 1];
+          v = f2_pack(__fsub_rn(__fmul_rn(e0, c), __fmul_rn(e1, s)),
+                      __fadd_rn(__fmul_rn(e0, s), __fmul_rn(e1, c)));
+        }
+      }
+    }
+    o0 = pack8_bf16_f2(y[0]);
+    o1 = pack8_bf16_f2(y[1]);
+  };
+
+  if (TO == kToRows || is_q) {
+    uint16_t* dst = (is_q ? a.q_out + row * a.ld_q : a.k_out + row * a.ld_k) + long(j0) * a.hd;
+#pragma unroll 1
+    for (int u = 0; u < jn; ++u, dst += a.hd) {
+      uint4 o0, o1;
+      advance(u, o0, o1);
+      norm_rotate(o0, o1);
       if (has0 && !bad_pos) *reinterpret_cast<uint4*>(dst + p0 * 8) = o0;
       if (has1 && !bad_pos) *reinterpret_cast<uint4*>(dst + p1 * 8) = o1;
-    } else {
-      const int kvh = is_v ? h - a.hq - a.hkv : h - a.hq;
-      const bool cached = slot >= 0 && !bad_slot && !bad_pos;   // the group's
-      if (!cached) continue;
-      uint8_t* rec = a.pool.record(slot, kvh);
-      const long row_in = a.pool.row(slot);
-      if constexpr (TO == kToBf16Pages) {
-        uint8_t* dst = rec + ((is_v ? a.pool.page_size : 0) + row_in) * a.hd * 2;
-        if (has0) *reinterpret_cast<uint4*>(dst + p0 * 16) = o0;
-        if (has1) *reinterpret_cast<uint4*>(dst + p1 * 16) = o1;
-      } else {
-        const float rk = __frcp_rn(*(is_v ? a.v_scale : a.k_scale));
-        const uint64_t rk2 = f2_pack(rk, rk);
-        uint64_t y[2][4];
-        unpack8_f2(o0, y[0]);  // what is cached is the bf16 key
-        unpack8_f2(o1, y[1]);
+    }
+    return;
+  }
+  if (slot < 0 || bad_slot || bad_pos) return;   // the group's
+  uint8_t* rec = a.pool.record(slot, j0);
+  const long row_in = a.pool.row(slot);
+  if constexpr (TO == kToBf16Pages) {
+    rec += ((is_v ? a.pool.page_size : 0) + row_in) * a.hd * 2;
+#pragma unroll 1
+    for (int u = 0; u < jn; ++u, rec += a.pool.record_bytes) {
+      uint4 o0, o1;
+      advance(u, o0, o1);
+      if (!is_v) norm_rotate(o0, o1);
+      if (has0) *reinterpret_cast<uint4*>(rec + p0 * 16) = o0;
+      if (has1) *reinterpret_cast<uint4*>(rec + p1 * 16) = o1;
+    }
+  }
+  if constexpr (TO == kToFp4Pages) {
+    const float rk = __frcp_rn(static_scale);
+    const uint64_t rk2 = f2_pack(rk, rk);
+    rec += is_v ? a.pool.record_bytes / 2 : 0;
+    const long scales = long(a.pool.page_size) * (a.hd / 2) + row_in * (a.hd / 16);
+    // a block of 16 is two neighbouring pieces: who holds the other
+    int lane0, lane1, slot0, slot1;
+    at.find(p0 ^ 1, &lane0, &slot0);
+    at.find(p1 ^ 1, &lane1, &slot1);
+#pragma unroll 1
+    for (int u = 0; u < jn; ++u, rec += a.pool.record_bytes) {
+      uint4 o0, o1;
+      advance(u, o0, o1);
+      if (!is_v) norm_rotate(o0, o1);
+      uint64_t y[2][4];
+      unpack8_f2(o0, y[0]);  // what is cached is the bf16 key
+      unpack8_f2(o1, y[1]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          y[0][j] = mul2(y[0][j], rk2);
-          y[1][j] = mul2(y[1][j], rk2);
-        }
-        // a block of 16 is two neighbouring pieces: the other one's largest
-        float big[2] = {absmax8(y[0]), absmax8(y[1])}, all[2];
+      for (int j = 0; j < 4; ++j) {
+        y[0][j] = mul2(y[0][j], rk2);
+        y[1][j] = mul2(y[1][j], rk2);
+      }
+      float big0 = absmax8(y[0]), big1 = absmax8(y[1]);
+      const float a0 = __shfl_sync(group, big0, lane0, LANES), a1 = __shfl_sync(group, big1, lane0, LANES);
+      const float b0 = __shfl_sync(group, big0, lane1, LANES), b1 = __shfl_sync(group, big1, lane1, LANES);
+      big0 = fmaxf(big0, slot0 ? a1 : a0);
+      big1 = fmaxf(big1, slot1 ? b1 : b0);
+      if (__any_sync(group, fmaxf(big0, big1) > 8192.0f)) {
+        // far past saturation: keeps infinities out of the remainder
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          int l, sl;
-          at.find((i ? p1 : p0) ^ 1, &l, &sl);
-          const float b0 = __shfl_sync(group, big[0], l, LANES), b1 = __shfl_sync(group, big[1], l, LANES);
-          all[i] = fmaxf(big[i], sl ? b1 : b0);
-        }
-        rec += is_v ? a.pool.record_bytes / 2 : 0;
-        uint8_t* scales = rec + long(a.pool.page_size) * (a.hd / 2) + row_in * (a.hd / 16);
-        rec += row_in * (a.hd / 2);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int p = i ? p1 : p0;
-          if (!(i ? has1 : has0)) continue;
-          uint8_t s8;
-          const uint32_t codes = quantise8(y[i], all[i], &s8);
-          *reinterpret_cast<uint32_t*>(rec + p * 4) = codes;
-          if ((p & 1) == 0) scales[p / 2] = s8;
+        for (int j = 0; j < 8; ++j) {
+          uint64_t& v = y[j / 4][j % 4];
+          v = f2_pack(fminf(fmaxf(f2_lo(v), -8192.0f), 8192.0f), fminf(fmaxf(f2_hi(v), -8192.0f), 8192.0f));
         }
       }
+      const uint8_t s0 = block_scale(big0), s1 = block_scale(big1);
+      uint8_t* codes = rec + row_in * (a.hd / 2);
+      if (has0) *reinterpret_cast<uint32_t*>(codes + p0 * 4) = quantise8(y[0], s0);
+      if (has1) *reinterpret_cast<uint32_t*>(codes + p1 * 4) = quantise8(y[1], s1);
+      if (has0 && (p0 & 1) == 0) rec[scales + p0 / 2] = s0;
+      if (has1 && (p1 & 1) == 0) rec[scales + p1 / 2] = s1;
     }
   }
 }
 
 template <int LANES, int U>
-int launch_heads(int to, const HeadArgs& a, cudaStream_t s) {
-  const long units = long(a.rows) * ((a.heads + U - 1) / U);
+int launch_heads(int to, HeadArgs a, cudaStream_t s) {
+  a.q_units = to == kToRows || a.q_out ? (a.hq + U - 1) / U : 0;
+  const long units = long(a.rows) * (a.q_units + (a.hkv + U - 1) / U * (to == kToRows ? 1 : 2));
   const long blocks = (units * LANES + 255) / 256;
   FRT_REQUIRE(units <= 0x7fffff00L, FRT_ESHAPE, "rows * heads is too large");
   const dim3 grid{unsigned(blocks)}, block{256};
@@ -357,10 +383,11 @@ int launch_heads(int to, const HeadArgs& a, cudaStream_t s) {
   // One head a group while the heads do not fill the GPU (latency), four
   // once they do (the table row and the index arithmetic are shared).
   const int lanes = a.hd <= 64 ? 4 : a.hd <= 128 ? 8 : 16;
-  const bool few = long(a.rows) * a.heads * lanes <= num_sms() * 2048L;
-  if (lanes == 4) return few ? launch_heads<4, 1>(to, a, s) : launch_heads<4, 4>(to, a, s);
-  if (lanes == 8) return few ? launch_heads<8, 1>(to, a, s) : launch_heads<8, 4>(to, a, s);
-  return few ? launch_heads<16, 1>(to, a, s) : launch_heads<16, 4>(to, a, s);
+  const bool few = long(a.rows) * (a.hq + 2 * a.hkv) * lanes <= num_sms() * 2048L;
+  constexpr int U = 4;
+  if (lanes == 4) return few ? launch_heads<4, 1>(to, a, s) : launch_heads<4, U>(to, a, s);
+  if (lanes == 8) return few ? launch_heads<8, 1>(to, a, s) : launch_heads<8, U>(to, a, s);
+  return few ? launch_heads<16, 1>(to, a, s) : launch_heads<16, U>(to, a, s);
 }
 
 // ------------------------------------------------------------------ read --
@@ -565,8 +592,6 @@ extern "C" int frt_qk_norm_rope(const frt_qk_rope_desc* d, void* stream) {
     if (int rc = frt::check_rows("k_out", d->k_out, d->ld_k, d->hkv * hd)) return rc;
   frt::HeadArgs a = frt::head_args(d);
   FRT_REQUIRE(a.status, FRT_ECUDA, "device status word unavailable");
-  a.first = 0;
-  a.heads = d->hq + d->hkv;
   return frt::launch_heads(frt::kToRows, a, static_cast<cudaStream_t>(stream));
 }
 
@@ -583,8 +608,6 @@ extern "C" int frt_paged_kv_append(const frt_qk_rope_desc* d, void* stream) {
   frt::HeadArgs a = frt::head_args(d);
   FRT_REQUIRE(a.status, FRT_ECUDA, "device status word unavailable");
   a.pool = frt::page_pool(d);
-  a.first = d->q_out ? 0 : d->hq;
-  a.heads = d->hq + 2 * d->hkv - a.first;
   return frt::launch_heads(d->format == FRT_PAGE_BF16 ? frt::kToBf16Pages : frt::kToFp4Pages, a,
                            static_cast<cudaStream_t>(stream));
 }
