@@ -12,6 +12,8 @@ namespace frt {
 constexpr uint64_t kAttnWaitNs = 2000000000ull;  // 2 s per wait
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+// stands for a score scale of 0, so that a hidden score (-inf) stays hidden
+constexpr float kTinyScale = 1e-30f;
 
 struct AttnArgs {
   int n_seqs, rows, max_q, hq, hkv, group, causal, window;

@@ -112,12 +112,13 @@ template <int HD, int NT>
 struct FewCfg {
   static constexpr int W = 4;                    // computing warps
   static constexpr int R = 8 * NT;               // query rows
-  static constexpr int CK = 16 * W;              // keys of a chunk
+  static constexpr int GR = NT == 1 ? 2 : 1;     // groups of 16 keys a warp takes at once
+  static constexpr int CK = 16 * GR * W;         // keys of a chunk
   static constexpr int kStage = CK * HD * 9 / 8; // bytes of a chunk
   static constexpr bool kQRegs = HD / 8 * NT <= 32;
   static constexpr int kJoin = W * R * HD * 4;   // the warps' sums when a unit ends
   static constexpr int kQBytes = kQRegs ? 0 : HD / 16 * NT * 32 * 8;
-  static constexpr int kStages = HD == 256 ? 4 : 6;
+  static constexpr int kStages = (HD == 256 ? 4 : 6) / GR;
   static constexpr int kThreads = 32 * (W + 1);
   static constexpr int kCtas = HD / 16 * NT <= 8 ? 3 : HD / 16 * NT <= 16 ? 2 : 1;  // per SM
   static constexpr int kTile = R * (HD + 2);     // floats of one partial state
@@ -128,7 +129,7 @@ template <int HD, int NT>
 __global__ void __launch_bounds__(FewCfg<HD, NT>::kThreads, FewCfg<HD, NT>::kCtas)
 attn_few_kernel(AttnArgs a) {
   using C = FewCfg<HD, NT>;
-  constexpr int W = C::W, R = C::R, CK = C::CK;
+  constexpr int W = C::W, R = C::R, CK = C::CK, GR = C::GR;
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t* ring = smem;
   float* join = reinterpret_cast<float*>(ring + C::kStages * C::kStage);
@@ -293,8 +294,28 @@ attn_few_kernel(AttnArgs a) {
   // that spreads both reads over the banks.
   const int key_s = (g & ~1) + ((g ^ (g >> 1)) & 1);
   const int key_o[2] = {2 * t + (t & 1), 2 * t + ((t & 1) ^ 1)};
-  const float kscale = *a.k_scale * a.sm_scale * kLog2e;
+  // the sign of the scale goes into Q, so that the largest score is that of
+  // the largest product
+  const float scale = *a.k_scale * a.sm_scale * kLog2e;
+  const float kscale = scale == 0.0f ? kTinyScale : fabsf(scale);
   const float vscale = *a.v_scale;
+  // where in a stage this lane's bytes of the warp's first group lie, and
+  // the way to the next group (in the next record's piece, if that is 16 keys)
+  int piece[C::GR];
+#pragma unroll
+  for (int u = 0; u < C::GR; ++u) piece[u] = ps < CK ? (warp * C::GR + u) * 16 / sub : 0;
+  const int in_piece = warp * C::GR * 16 - piece[0] * sub;
+  const int at_rec = piece[0] * (sub * HD * 9 / 8);
+  const int at_k = at_rec + (in_piece + key_s) * (HD / 2) + t * (HD / 8);
+  const int at_ks = at_rec + sub * (HD / 2) + (in_piece + key_s) * (HD / 16) + t * (HD / 64);
+  int at_v[2], at_vs[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    at_v[k] = at_rec + sub * (HD / 2 + HD / 16) + (in_piece + key_o[k]) * (HD / 2) + g * (HD / 16);
+    at_vs[k] = at_rec + sub * (HD + HD / 16) + (in_piece + key_o[k]) * (HD / 16) + g * HD / 128;
+  }
+  const int code_step = sub == 16 ? 16 * HD * 9 / 8 : 16 * (HD / 2);
+  const int scale_step = sub == 16 ? 16 * HD * 9 / 8 : 16 * (HD / 16);
   int stage = 0;
   uint32_t phase = 0;
 
@@ -339,7 +360,7 @@ attn_few_kernel(AttnArgs a) {
       big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
       int e = int(__float_as_uint(big) >> 23);  // 2^(e - 127) <= big
       if (e < 1 || e > 253) e = 127;            // zero, subnormal, infinite: as it is
-      const float down = __uint_as_float(uint32_t(254 - e) << 23);
+      const float down = copysignf(__uint_as_float(uint32_t(254 - e) << 23), scale);
       const float up = __uint_as_float(uint32_t(e) << 23);
 #pragma unroll
       for (int i = 0; i < HD / 8; ++i) {
@@ -401,95 +422,107 @@ attn_few_kernel(AttnArgs a) {
         for (int j = 0; j < 4; ++j) o_acc[nt][i][j] = 0.0f;
 
     for (int n = 0; n < n_here; ++n, ++x) {
-      const int key0 = (w.q.chunk0 + w.chunk + n) * CK + warp * 16;
+      const int key0 = (w.q.chunk0 + w.chunk + n) * CK + warp * 16 * GR;
       // every lane waits: each reads what the copies wrote
       const bool got = mbar_wait_bounded(&full[stage], phase, kAttnWaitNs, abort_flag);
       if (!got && lane == 0) {
         atomicExch(a.status, FRT_ETIMEOUT);
         *abort_flag = 1;
       }
-      const int piece = ps < CK ? warp * 16 / sub : 0;
-      if (__all_sync(0xffffffffu, got) && key0 < tile_hi && key0 + 16 > tile_lo &&
-          (valid[stage] >> piece & 1)) {
-        const uint8_t* kc = ring + stage * C::kStage + piece * (sub * HD * 9 / 8);
-        const int at = warp * 16 - piece * sub;
-        const uint8_t* ks = kc + sub * (HD / 2) + at * (HD / 16);
-        const uint8_t* vc = kc + sub * (HD / 2 + HD / 16) + at * (HD / 2);
-        const uint8_t* vs = kc + sub * (HD + HD / 16) + at * (HD / 16);
-        kc += at * (HD / 2);
-        const bool masked = key0 + 16 > all_hi || key0 < all_lo;
-
-        // S^T, 16 keys x 8 NT rows
-        uint32_t kw[2][HD / 32];
-        uint32_t kscl[2][(HD + 127) / 128];  // pairs of block scales, fp16
+      if (__all_sync(0xffffffffu, got) && key0 < tile_hi && key0 + 16 * GR > tile_lo) {
+        const uint8_t* st = ring + stage * C::kStage;
+        const uint32_t have = valid[stage];
+        bool hidden[GR], masked = key0 + 16 * GR > all_hi || key0 < all_lo;
 #pragma unroll
-        for (int f = 0; f < 2; ++f) {
-          lds<HD / 8>(kc + (key_s + 8 * f) * (HD / 2) + t * (HD / 8), kw[f]);
-          const uint8_t* sp = ks + (key_s + 8 * f) * (HD / 16) + t * (HD / 64);
-          if constexpr (HD == 64) {
-            kscl[f][0] = e4m3x2_to_f16(*sp);
-          } else if constexpr (HD == 128) {
-            kscl[f][0] = e4m3x2_to_f16(*reinterpret_cast<const uint16_t*>(sp));
-          } else {
-            const uint32_t v = *reinterpret_cast<const uint32_t*>(sp);
-            kscl[f][0] = e4m3x2_to_f16(v & 0xFFFFu);
-            kscl[f][1] = e4m3x2_to_f16(v >> 16);
-          }
+        for (int u = 0; u < GR; ++u) {  // in a bad page
+          hidden[u] = !(have >> piece[u] & 1);
+          masked |= hidden[u];
         }
-        float s[NT][4];
+
+        // S^T, 16 GR keys x 8 NT rows
+        float s[GR][NT][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[nt][i] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < HD / 32; ++i) {  // 8 codes of each key: half a block
-          uint32_t h[2][4];
+        for (int u = 0; u < GR; ++u) {
+          uint32_t kw[2][HD / 32];
+          uint32_t kscl[2][(HD + 127) / 128];  // pairs of block scales, fp16
 #pragma unroll
           for (int f = 0; f < 2; ++f) {
-            e2m1x8_to_f16(kw[f][i], h[f]);
-            const uint32_t pair = kscl[f][i / 4];
-            const uint32_t sc = __byte_perm(pair, 0, i / 2 % 2 ? 0x3232 : 0x1010);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) h[f][k] = hmul2(h[f][k], sc);
+            lds<HD / 8>(st + at_k + u * code_step + f * (8 * HD / 2), kw[f]);
+            const uint8_t* sp = st + at_ks + u * scale_step + f * (8 * HD / 16);
+            if constexpr (HD == 64) {
+              kscl[f][0] = e4m3x2_to_f16(*sp);
+            } else if constexpr (HD == 128) {
+              kscl[f][0] = e4m3x2_to_f16(*reinterpret_cast<const uint16_t*>(sp));
+            } else {
+              const uint32_t v = *reinterpret_cast<const uint32_t*>(sp);
+              kscl[f][0] = e4m3x2_to_f16(v & 0xFFFFu);
+              kscl[f][1] = e4m3x2_to_f16(v >> 16);
+            }
           }
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              uint32_t b0, b1;
-              if constexpr (C::kQRegs) {
-                b0 = qf[nt][4 * i + 2 * k];
-                b1 = qf[nt][4 * i + 2 * k + 1];
-              } else {
-                const uint2 b = q_smem[(nt * (HD / 16) + 2 * i + k) * 32 + lane];
-                b0 = b.x; b1 = b.y;
-              }
-              mma_f16(s[nt], h[0][2 * k], h[1][2 * k], h[0][2 * k + 1], h[1][2 * k + 1], b0, b1);
+            for (int i = 0; i < 4; ++i) s[u][nt][i] = 0.0f;
+#pragma unroll
+          for (int i = 0; i < HD / 32; ++i) {  // 8 codes of each key: half a block
+            uint32_t h[2][4];
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+              e2m1x8_to_f16(kw[f][i], h[f]);
+              const uint32_t sc = __byte_perm(kscl[f][i / 4], 0, i / 2 % 2 ? 0x3232 : 0x1010);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) h[f][k] = hmul2(h[f][k], sc);
             }
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                uint32_t b0, b1;
+                if constexpr (C::kQRegs) {
+                  b0 = qf[nt][4 * i + 2 * k];
+                  b1 = qf[nt][4 * i + 2 * k + 1];
+                } else {
+                  const uint2 b = q_smem[(nt * (HD / 16) + 2 * i + k) * 32 + lane];
+                  b0 = b.x; b1 = b.y;
+                }
+                mma_f16(s[u][nt], h[0][2 * k], h[1][2 * k], h[0][2 * k + 1], h[1][2 * k + 1], b0, b1);
+              }
+          }
         }
 
         // softmax: base-2 scores against a running maximum that is raised
         // only when a score passes it by more than 2^8 (the weights then
         // stay within fp16), so most groups pass without the reduction
+        if (masked) {
+#pragma unroll
+          for (int u = 0; u < GR; ++u)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int key = key0 + 16 * u + key_s + 8 * (i >> 1);
+                if (hidden[u] || key >= lim_hi[nt][i & 1] || key < lim_lo[nt][i & 1])
+                  s[u][nt][i] = -INFINITY;
+              }
+        }
+        float top[NT][2];
         bool grow = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float v = s[nt][i] * cq[nt][i & 1];
-            if (masked) {
-              const int key = key0 + key_s + 8 * (i >> 1);
-              if (key >= lim_hi[nt][i & 1] || key < lim_lo[nt][i & 1]) v = -INFINITY;
-            }
-            s[nt][i] = v;
-            grow |= v > m[nt][i & 1] + 8.0f;
+          for (int e2 = 0; e2 < 2; ++e2) {
+            float v = fmaxf(s[0][nt][e2], s[0][nt][e2 + 2]);
+#pragma unroll
+            for (int u = 1; u < GR; ++u) v = fmaxf(v, fmaxf(s[u][nt][e2], s[u][nt][e2 + 2]));
+            top[nt][e2] = v == -INFINITY ? v : v * cq[nt][e2];
+            grow |= top[nt][e2] > m[nt][e2] + 8.0f;
           }
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e2 = 0; e2 < 2; ++e2) {
-              float v = fmaxf(s[nt][e2], s[nt][e2 + 2]);
+              float v = top[nt][e2];
 #pragma unroll
               for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
               v = fmaxf(v, m[nt][e2]);
@@ -503,61 +536,66 @@ attn_few_kernel(AttnArgs a) {
               }
             }
         }
-        uint32_t p[NT][2];
+        uint32_t p[GR][NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
+          const float base[2] = {m[nt][0] == -INFINITY ? 0.0f : -m[nt][0],
+                                 m[nt][1] == -INFINITY ? 0.0f : -m[nt][1]};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float mm = m[nt][i & 1];
-            s[nt][i] = ex2(s[nt][i] - (mm == -INFINITY ? 0.0f : mm));
-            l[nt][i & 1] += s[nt][i];
+          for (int u = 0; u < GR; ++u) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              s[u][nt][i] = ex2(fmaf(s[u][nt][i], cq[nt][i & 1], base[i & 1]));
+              l[nt][i & 1] += s[u][nt][i];
+            }
+            p[u][nt][0] = movmatrix_trans(pack_f16x2(s[u][nt][0], s[u][nt][1]));
+            p[u][nt][1] = movmatrix_trans(pack_f16x2(s[u][nt][2], s[u][nt][3]));
           }
-          p[nt][0] = movmatrix_trans(pack_f16x2(s[nt][0], s[nt][1]));
-          p[nt][1] = movmatrix_trans(pack_f16x2(s[nt][2], s[nt][3]));
         }
 
         // O^T += V^T P^T
-        uint32_t vw[2][2][HD / 64];       // [eight][key][words]
-        uint32_t vscl[2][HD == 256 ? 2 : 1];  // (key 0, key 1) scales, fp16
 #pragma unroll
-        for (int f = 0; f < 2; ++f) {
-          uint32_t sb[2];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int key = key_o[k] + 8 * f;
-            lds<HD / 16>(vc + key * (HD / 2) + g * (HD / 16), vw[f][k]);
-            const uint8_t* sp = vs + key * (HD / 16);
-            if constexpr (HD == 64) sb[k] = sp[g / 2];
-            else if constexpr (HD == 128) sb[k] = sp[g];
-            else sb[k] = *reinterpret_cast<const uint16_t*>(sp + 2 * g);
-            // behind the sequence's end the page may hold anything
-            if (masked && key0 + key >= w.q.L) sb[k] = 0;
-          }
-          vscl[f][0] = e4m3x2_to_f16(__byte_perm(sb[0], sb[1], 0x0040));
-          if constexpr (HD == 256) vscl[f][1] = e4m3x2_to_f16(__byte_perm(sb[0], sb[1], 0x0051));
-        }
-#pragma unroll
-        for (int i = 0; i < HD / 64; ++i) {  // 8 elements of every key
-          uint32_t even[2][4], odd[2][4];
+        for (int u = 0; u < GR; ++u) {
+          uint32_t vw[2][2][HD / 64];       // [eight][key][words]
+          uint32_t vscl[2][HD == 256 ? 2 : 1];  // (key 0, key 1) scales, fp16
 #pragma unroll
           for (int f = 0; f < 2; ++f) {
-            const uint32_t w0 = vw[f][0][i], w1 = vw[f][1][i];
-            constexpr uint32_t kLow = 0x0F0F0F0Fu;
-            e2m1x8_to_f16((w0 & kLow) | ((w1 << 4) & ~kLow), even[f]);
-            e2m1x8_to_f16(((w0 >> 4) & kLow) | (w1 & ~kLow), odd[f]);
-            const uint32_t sc = vscl[f][HD == 256 ? i / 2 : 0];
+            uint32_t sb[2];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              even[f][k] = hmul2(even[f][k], sc);
-              odd[f][k] = hmul2(odd[f][k], sc);
+            for (int k = 0; k < 2; ++k) {
+              lds<HD / 16>(st + at_v[k] + u * code_step + f * (8 * HD / 2), vw[f][k]);
+              const uint8_t* sp = st + at_vs[k] + u * scale_step + f * (8 * HD / 16);
+              if constexpr (HD == 256) sb[k] = *reinterpret_cast<const uint16_t*>(sp);
+              else sb[k] = *sp;
+              // behind the sequence's end the page may hold anything
+              if (masked && (hidden[u] || key0 + 16 * u + key_o[k] + 8 * f >= w.q.L)) sb[k] = 0;
             }
+            vscl[f][0] = e4m3x2_to_f16(__byte_perm(sb[0], sb[1], 0x0040));
+            if constexpr (HD == 256) vscl[f][1] = e4m3x2_to_f16(__byte_perm(sb[0], sb[1], 0x0051));
           }
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
+          for (int i = 0; i < HD / 64; ++i) {  // 8 elements of every key
+            uint32_t even[2][4], odd[2][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma_f16(o_acc[nt][4 * i + k], even[0][k], odd[0][k], even[1][k], odd[1][k],
-                      p[nt][0], p[nt][1]);
+            for (int f = 0; f < 2; ++f) {
+              const uint32_t w0 = vw[f][0][i], w1 = vw[f][1][i];
+              constexpr uint32_t kLow = 0x0F0F0F0Fu;
+              e2m1x8_to_f16((w0 & kLow) | ((w1 << 4) & ~kLow), even[f]);
+              e2m1x8_to_f16(((w0 >> 4) & kLow) | (w1 & ~kLow), odd[f]);
+              const uint32_t sc = vscl[f][HD == 256 ? i / 2 : 0];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                even[f][k] = hmul2(even[f][k], sc);
+                odd[f][k] = hmul2(odd[f][k], sc);
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma_f16(o_acc[nt][4 * i + k], even[0][k], odd[0][k], even[1][k], odd[1][k],
+                        p[u][nt][0], p[u][nt][1]);
+          }
         }
       }
       __syncwarp();

@@ -247,7 +247,7 @@ attn_many_kernel(AttnArgs a, int splits, int tiles_max) {
     // the largest product
     const float scale = *a.k_scale * a.sm_scale * kLog2e;
     const float down = copysignf(__uint_as_float(uint32_t(254 - e) << 23), scale);
-    const float c = fabsf(scale) * __uint_as_float(uint32_t(e) << 23);
+    const float c = (scale == 0.0f ? kTinyScale : fabsf(scale)) * __uint_as_float(uint32_t(e) << 23);
 #pragma unroll 8
     for (int i = 0; i < HD / 8; ++i) {
       float f[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};

@@ -188,6 +188,14 @@ def test_peaked_and_far_scores(rt):
         p.check()
 
 
+@pytest.mark.parametrize("Lq", [1, 60])
+def test_scale_of_zero(rt, Lq):
+    """Every visible key weighs the same."""
+    p = Problem(rt, np.random.default_rng(20), [(Lq, 150), (1, 70)], 4, 2, 64, 16, scale=0.0)
+    p.run()
+    p.check()
+
+
 def test_one_long_sequence(rt):
     rng = np.random.default_rng(9)
     p = Problem(rt, rng, [(1, 40000)], 8, 2, 128, 64)
