@@ -14,6 +14,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // stands for a score scale of 0, so that a hidden score (-inf) stays hidden
 constexpr float kTinyScale = 1e-30f;
+// the running maximum of a row that has seen no key
+constexpr float kNoKey = -1e30f;
 
 struct AttnArgs {
   int n_seqs, rows, max_q, hq, hkv, group, causal, window;

@@ -41,9 +41,9 @@ struct Walker {
   Seq q;
   int s, unit, chunk;   // unit = tile * hkv + head
 
-  __device__ void start(const AttnArgs& a, int seq, long offset) {
-    s = seq;
-    q = load_seq<R, CK>(a, s, false);
+  __device__ void begin(const Seq& seq, int index, long offset) {
+    s = index;
+    q = seq;
     unit = int(offset / q.chunks);
     chunk = int(offset - long(unit) * q.chunks);
   }
@@ -61,7 +61,7 @@ struct Walker {
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
       " {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -115,7 +115,7 @@ struct FewCfg {
   static constexpr int GR = NT == 1 ? 2 : 1;     // groups of 16 keys a warp takes at once
   static constexpr int CK = 16 * GR * W;         // keys of a chunk
   static constexpr int kStage = CK * HD * 9 / 8; // bytes of a chunk
-  static constexpr bool kQRegs = HD / 8 * NT <= 32;
+  static constexpr bool kQRegs = HD * NT < 128;
   static constexpr int kJoin = W * R * HD * 4;   // the warps' sums when a unit ends
   static constexpr int kQBytes = kQRegs ? 0 : HD / 16 * NT * 32 * 8;
   static constexpr int kStages = (HD == 256 ? 4 : 6) / GR;
@@ -142,6 +142,7 @@ attn_few_kernel(AttnArgs a) {
   long* scan = reinterpret_cast<long*>(valid + 8);    // [kThreads / 32] and the start
   volatile int* abort_flag = reinterpret_cast<volatile int*>(scan + 8);
   int* last = reinterpret_cast<int*>(scan + 8) + 1;
+  Seq* start = reinterpret_cast<Seq*>(scan + 9);
 
   const int tid = int(threadIdx.x), warp = tid / 32, lane = tid % 32;
   pdl_trigger();
@@ -158,10 +159,15 @@ attn_few_kernel(AttnArgs a) {
 
   // --- this CTA's run of the line of all chunks ---
   long total = 0, upto = 0;
+  Seq mine;
+  mine.tiles = mine.chunks = 0;
   for (int base = 0; base < a.n_seqs; base += C::kThreads) {
     const int s = base + tid;
     long n = 0;
-    if (s < a.n_seqs) n = load_seq<R, CK>(a, s, blockIdx.x == 0).work(a.hkv);
+    if (s < a.n_seqs) {
+      mine = load_seq<R, CK>(a, s, blockIdx.x == 0);
+      n = mine.work(a.hkv);
+    }
     long inc = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -189,7 +195,11 @@ attn_few_kernel(AttnArgs a) {
     for (int base = 0; base < a.n_seqs; base += C::kThreads) {
       const int s = base + tid;
       long n = 0;
-      if (s < a.n_seqs) n = load_seq<R, CK>(a, s, false).work(a.hkv);
+      Seq q;
+      if (s < a.n_seqs) {
+        q = load_seq<R, CK>(a, s, false);
+        n = q.work(a.hkv);
+      }
       long inc = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -208,19 +218,21 @@ attn_few_kernel(AttnArgs a) {
       if (n > 0 && begin >= hi - n && begin < hi) {
         scan[6] = s;
         scan[7] = begin - (hi - n);
+        *start = q;
       }
       run += all;
     }
   } else if (tid < a.n_seqs) {
-    const long n = load_seq<R, CK>(a, tid, false).work(a.hkv);
+    const long n = mine.work(a.hkv);
     if (n > 0 && begin >= upto - n && begin < upto) {
       scan[6] = tid;
       scan[7] = begin - (upto - n);
+      *start = mine;
     }
   }
   __syncthreads();
   Walker<R, CK> w;
-  w.start(a, int(scan[6]), scan[7]);
+  w.begin(*start, int(scan[6]), scan[7]);
 
   const int ps = a.pool.page_size;
   const int sub = ps < CK ? ps : CK;  // keys of one record's piece in a chunk
@@ -232,18 +244,28 @@ attn_few_kernel(AttnArgs a) {
     const int n_sub = CK / sub;
     const bool parts = ps > CK;
     long issued = 0;
-    for (long x = begin; x < end; ++x) {
-      const int head = w.unit % a.hkv;
+    // lane i looks up piece i of the chunk the walker stands at: one chunk
+    // ahead, so that the table's latency is not in the way of the copies
+    auto look_up = [&]() {
       const int key0 = (w.q.chunk0 + w.chunk) * CK;
-      // lane i: piece i of the chunk
-      const int piece_key = parts ? key0 : key0 + lane * sub;
-      int page = -1;
-      if (lane < (parts ? 4 : n_sub) && piece_key < w.q.L) {
-        page = a.page_table[long(w.s) * a.max_pages + (piece_key >> a.pool.shift)];
-        if (page < 0 || page >= a.pool.n_pages) {
-          atomicExch(a.status, FRT_ERANGE);
-          page = -1;
-        }
+      const int key = parts ? key0 : key0 + lane * sub;
+      if (lane >= (parts ? 4 : n_sub) || key >= w.q.L) return -1;
+      return __ldg(a.page_table + long(w.s) * a.max_pages + (key >> a.pool.shift));
+    };
+    int page_next = look_up();
+    for (long x = begin; x < end; ++x) {
+      int page = page_next;
+      const int head = w.unit % a.hkv;
+      const int at = (w.q.chunk0 + w.chunk) * CK & (ps - 1);
+      const bool in_range = lane < (parts ? 4 : n_sub) &&
+                            (w.q.chunk0 + w.chunk) * CK + (parts ? 0 : lane * sub) < w.q.L;
+      if (x + 1 < end) {
+        if (++w.chunk == w.q.chunks) w.next_unit(a);
+        page_next = look_up();
+      }
+      if (in_range && (page < 0 || page >= a.pool.n_pages)) {
+        atomicExch(a.status, FRT_ERANGE);
+        page = -1;
       }
       const uint32_t have = __ballot_sync(0xffffffffu, page >= 0);
       bool ok = true;
@@ -268,7 +290,6 @@ attn_few_kernel(AttnArgs a) {
         if (!parts) {
           bulk_load(dst + lane * (sub * HD * 9 / 8), rec, sub * HD * 9 / 8, &full[stage]);
         } else {  // lane 0 .. 3: key codes, key scales, value codes, value scales
-          const int at = key0 & (ps - 1);
           rec += (lane & 2 ? a.pool.record_bytes / 2 : 0) +
                  (lane & 1 ? ps * (HD / 2) + at * (HD / 16) : at * (HD / 2));
           dst += (lane & 2 ? C::kStage / 2 : 0) + (lane & 1 ? CK * (HD / 2) : 0);
@@ -277,7 +298,6 @@ attn_few_kernel(AttnArgs a) {
       }
       ++issued;
       if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
-      if (++w.chunk == w.q.chunks && x + 1 < end) w.next_unit(a);
     }
     // after a wait that ran out: no exit with copies in flight
     if (*abort_flag && lane == 0) {
@@ -403,7 +423,7 @@ attn_few_kernel(AttnArgs a) {
         }
         lim_hi[nt][e2] = hi;
         lim_lo[nt][e2] = lo;
-        m[nt][e2] = -INFINITY;
+        m[nt][e2] = kNoKey;
         l[nt][e2] = 0.0f;
       }
 #pragma unroll
@@ -514,7 +534,7 @@ attn_few_kernel(AttnArgs a) {
             float v = fmaxf(s[0][nt][e2], s[0][nt][e2 + 2]);
 #pragma unroll
             for (int u = 1; u < GR; ++u) v = fmaxf(v, fmaxf(s[u][nt][e2], s[u][nt][e2 + 2]));
-            top[nt][e2] = v == -INFINITY ? v : v * cq[nt][e2];
+            top[nt][e2] = v * cq[nt][e2];
             grow |= top[nt][e2] > m[nt][e2] + 8.0f;
           }
         if (__any_sync(0xffffffffu, grow)) {
@@ -526,7 +546,7 @@ attn_few_kernel(AttnArgs a) {
 #pragma unroll
               for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
               v = fmaxf(v, m[nt][e2]);
-              const float f = v == -INFINITY ? 1.0f : ex2(m[nt][e2] - v);
+              const float f = ex2(m[nt][e2] - v);
               m[nt][e2] = v;
               l[nt][e2] *= f;
 #pragma unroll
@@ -539,13 +559,11 @@ attn_few_kernel(AttnArgs a) {
         uint32_t p[GR][NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const float base[2] = {m[nt][0] == -INFINITY ? 0.0f : -m[nt][0],
-                                 m[nt][1] == -INFINITY ? 0.0f : -m[nt][1]};
 #pragma unroll
           for (int u = 0; u < GR; ++u) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              s[u][nt][i] = ex2(fmaf(s[u][nt][i], cq[nt][i & 1], base[i & 1]));
+              s[u][nt][i] = ex2(fmaf(s[u][nt][i], cq[nt][i & 1], -m[nt][i & 1]));
               l[nt][i & 1] += s[u][nt][i];
             }
             p[u][nt][0] = movmatrix_trans(pack_f16x2(s[u][nt][0], s[u][nt][1]));
@@ -567,8 +585,11 @@ attn_few_kernel(AttnArgs a) {
               const uint8_t* sp = st + at_vs[k] + u * scale_step + f * (8 * HD / 16);
               if constexpr (HD == 256) sb[k] = *reinterpret_cast<const uint16_t*>(sp);
               else sb[k] = *sp;
-              // behind the sequence's end the page may hold anything
-              if (masked && (hidden[u] || key0 + 16 * u + key_o[k] + 8 * f >= w.q.L)) sb[k] = 0;
+            }
+            if (masked) {  // behind the sequence's end the page may hold anything
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+                if (hidden[u] || key0 + 16 * u + key_o[k] + 8 * f >= w.q.L) sb[k] = 0;
             }
             vscl[f][0] = e4m3x2_to_f16(__byte_perm(sb[0], sb[1], 0x0040));
             if constexpr (HD == 256) vscl[f][1] = e4m3x2_to_f16(__byte_perm(sb[0], sb[1], 0x0051));
@@ -638,13 +659,13 @@ attn_few_kernel(AttnArgs a) {
     const long final = ((unit0 + w.q.chunks) * ctas - 1) / total;
     for (int i = tid; i < R * (HD / 4); i += W * 32) {
       const int r = i / (HD / 4), d = i % (HD / 4) * 4;
-      float mm = -INFINITY, ll = 0.0f;
+      float mm = kNoKey, ll = 0.0f;
 #pragma unroll
       for (int k = 0; k < W; ++k) mm = fmaxf(mm, join_m[k * R + r]);
       float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
       for (int k = 0; k < W; ++k) {
-        const float f = mm == -INFINITY ? 0.0f : ex2(join_m[k * R + r] - mm);
+        const float f = ex2(join_m[k * R + r] - mm);
         const float4 v = *reinterpret_cast<const float4*>(join + (k * R + r) * HD + d);
         ll += join_l[k * R + r] * f;
         acc.x += v.x * f; acc.y += v.y * f; acc.z += v.z * f; acc.w += v.w * f;
@@ -664,7 +685,7 @@ attn_few_kernel(AttnArgs a) {
       *reinterpret_cast<uint2*>(a.out + long(w.q.r0 + token) * a.ld_out + long(h) * HD + d) =
           make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
       if (d == 0 && a.lse)
-        a.lse[long(w.q.r0 + token) * a.hq + h] = mm == -INFINITY ? mm : (mm + log2f(ll)) * kLn2;
+        a.lse[long(w.q.r0 + token) * a.hq + h] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * kLn2;
     }
     if (!whole) {
       __threadfence();
@@ -681,14 +702,14 @@ attn_few_kernel(AttnArgs a) {
           const int r = i / (HD / 4), d = i % (HD / 4) * 4;
           const int row = tile * R + r;
           if (row >= rows_here) continue;
-          float mm = -INFINITY, ll = 0.0f;
+          float mm = kNoKey, ll = 0.0f;
           for (long k = first; k <= final; ++k)
             mm = fmaxf(mm, __ldcg(a.partials + (2 * k + (k == first)) * C::kTile + R * HD + r));
           float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
           for (long k = first; k <= final; ++k) {
             const float* pt = a.partials + (2 * k + (k == first)) * C::kTile;
-            const float f = mm == -INFINITY ? 0.0f : ex2(__ldcg(pt + R * HD + r) - mm);
+            const float f = ex2(__ldcg(pt + R * HD + r) - mm);
             const float4 v = __ldcg(reinterpret_cast<const float4*>(pt + r * HD + d));
             ll += __ldcg(pt + R * HD + R + r) * f;
             acc.x += v.x * f; acc.y += v.y * f; acc.z += v.z * f; acc.w += v.w * f;
@@ -699,7 +720,7 @@ attn_few_kernel(AttnArgs a) {
               make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv),
                          pack_bf16x2(acc.z * inv, acc.w * inv));
           if (d == 0 && a.lse)
-            a.lse[long(w.q.r0 + token) * a.hq + h] = mm == -INFINITY ? mm : (mm + log2f(ll)) * kLn2;
+            a.lse[long(w.q.r0 + token) * a.hq + h] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * kLn2;
         }
       }
     }

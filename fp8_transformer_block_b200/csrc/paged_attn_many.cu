@@ -229,33 +229,49 @@ attn_many_kernel(AttnArgs a, int splits, int tiles_max) {
     const int h = head * a.group + (live ? row - token * a.group : 0);
     const uint32_t lane_base = tmem + (uint32_t(warp % 4 * 32) << 16);
 
-    // Q: fp16 under a power of two that brings the row's largest below 2
-    const uint16_t* src = a.q + long(q.r0 + token) * a.ld_q + long(h) * HD;
-    float big = 0.0f;
-    if (live) {
-#pragma unroll 8
-      for (int i = 0; i < HD / 8; ++i) {
-        float f[8];
-        unpack8(reinterpret_cast<const uint4*>(src)[i], f);
+    // Q: fp16 under a power of two that brings the row's largest below 2.
+    // HD / 8 lanes read a row (16 bytes each), 4 batches of 8 warp loads.
+    const float scale = *a.k_scale * a.sm_scale * kLog2e;
+    constexpr int kLanes = HD / 8, kRows = 32 / kLanes;   // rows of a warp load
+    constexpr int kBatch = HD == 256 ? 16 : HD == 128 ? 16 : 8;
+    float c = 0.0f;
+#pragma unroll 1
+    for (int base = 0; base < 32 / kRows; base += kBatch) {
+      uint4 raw[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int x = tile * R + t * 128 + warp % 4 * 32 + (base + i) * kRows + lane / kLanes;
+        const int tok = x / a.group;
+        raw[i] = make_uint4(0, 0, 0, 0);
+        if (x < q.Lq * a.group)
+          raw[i] = *reinterpret_cast<const uint4*>(a.q + long(q.r0 + tok) * a.ld_q +
+                                                   long(head * a.group + x - tok * a.group) * HD +
+                                                   lane % kLanes * 8);
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        float f[8], big = 0.0f;
+        unpack8(raw[i], f);
 #pragma unroll
         for (int k = 0; k < 8; ++k) big = fmaxf(big, fabsf(f[k]));
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+        int e = int(__float_as_uint(big) >> 23);
+        if (e < 1 || e > 253) e = 127;
+        // the sign of the scale goes into Q, so that the largest score is that
+        // of the largest product
+        const float down = copysignf(__uint_as_float(uint32_t(254 - e) << 23), scale);
+        const int rr = warp % 4 * 32 + (base + i) * kRows + lane / kLanes, col = lane % kLanes;
+        *reinterpret_cast<uint4*>(q_s + t * C::kQBytes + col / 8 * (128 * 128) + rr * 128 +
+                                  ((col % 8) ^ (rr & 7)) * 16) =
+            make_uint4(pack_f16x2(f[0] * down, f[1] * down), pack_f16x2(f[2] * down, f[3] * down),
+                       pack_f16x2(f[4] * down, f[5] * down), pack_f16x2(f[6] * down, f[7] * down));
+        // the row's own thread keeps its factor
+        const float up = __uint_as_float(uint32_t(e) << 23);
+        const int own = lane - (base + i) * kRows;
+        const float theirs = __shfl_sync(0xffffffffu, up, own >= 0 && own < kRows ? own * kLanes : 0);
+        if (own >= 0 && own < kRows) c = theirs * (scale == 0.0f ? kTinyScale : fabsf(scale));
       }
-    }
-    int e = int(__float_as_uint(big) >> 23);
-    if (e < 1 || e > 253) e = 127;
-    // the sign of the scale goes into Q, so that the largest score is that of
-    // the largest product
-    const float scale = *a.k_scale * a.sm_scale * kLog2e;
-    const float down = copysignf(__uint_as_float(uint32_t(254 - e) << 23), scale);
-    const float c = (scale == 0.0f ? kTinyScale : fabsf(scale)) * __uint_as_float(uint32_t(e) << 23);
-#pragma unroll 8
-    for (int i = 0; i < HD / 8; ++i) {
-      float f[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-      if (live) unpack8(reinterpret_cast<const uint4*>(src)[i], f);
-      const uint4 o = make_uint4(pack_f16x2(f[0] * down, f[1] * down), pack_f16x2(f[2] * down, f[3] * down),
-                                 pack_f16x2(f[4] * down, f[5] * down), pack_f16x2(f[6] * down, f[7] * down));
-      *reinterpret_cast<uint4*>(q_s + t * C::kQBytes + i / 8 * (128 * 128) + r * 128 +
-                                ((i % 8) ^ (r & 7)) * 16) = o;
     }
     fence_proxy_async_smem();
     mbar_arrive(&q_full[t]);
@@ -400,28 +416,34 @@ attn_many_kernel(AttnArgs a, int splits, int tiles_max) {
     constexpr int kPieces = KVT * HD / 32;       // 32 codes and two scales
     constexpr int kMine = kPieces / C::kWide;
     const int ps = a.pool.page_size;
-    uint4 code[kMine];
-    uint32_t scl[kMine];
-    auto load = [&](int j, int half) {           // half 0: keys, 1: values
+    // codes and scales of this thread's pieces of the next K and V tile, and
+    // the pages of the tile after it: no load is waited for where it is issued
+    uint4 k_code[kMine], v_code[kMine];
+    uint32_t k_scl[kMine], v_scl[kMine];
+    int page[kMine];
+    auto look_up = [&](int j) {
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const int key = j * KVT + (i * C::kWide + wt) / (HD / 32);
+        page[i] = key < q.L ? __ldg(a.page_table + long(s) * a.max_pages + (key >> a.pool.shift)) : -1;
+      }
+    };
+    auto load = [&](int j, int half, uint4 (&code)[kMine], uint32_t (&scl)[kMine]) {
 #pragma unroll
       for (int i = 0; i < kMine; ++i) {
         const int flat = i * C::kWide + wt;
-        const int key = j * KVT + flat / (HD / 32), piece = flat % (HD / 32);
+        const int at = (j * KVT + flat / (HD / 32)) & (ps - 1), piece = flat % (HD / 32);
         code[i] = make_uint4(0, 0, 0, 0);
         scl[i] = 0;
-        if (key < q.L) {
-          const int page = a.page_table[long(s) * a.max_pages + (key >> a.pool.shift)];
-          if (page >= 0 && page < a.pool.n_pages) {
-            const int at = key & (ps - 1);
-            const uint8_t* rec = a.pool.base + (long(page) * a.pool.hkv + head) * a.pool.record_bytes +
-                                 half * (a.pool.record_bytes / 2);
-            code[i] = __ldg(reinterpret_cast<const uint4*>(rec + at * (HD / 2) + piece * 16));
-            scl[i] = __ldg(reinterpret_cast<const uint16_t*>(rec + ps * (HD / 2) + at * (HD / 16) + piece * 2));
-          }
+        if (page[i] >= 0 && page[i] < a.pool.n_pages) {
+          const uint8_t* rec = a.pool.base + (long(page[i]) * a.pool.hkv + head) * a.pool.record_bytes +
+                               half * (a.pool.record_bytes / 2);
+          code[i] = __ldg(reinterpret_cast<const uint4*>(rec + at * (HD / 2) + piece * 16));
+          scl[i] = __ldg(reinterpret_cast<const uint16_t*>(rec + ps * (HD / 2) + at * (HD / 16) + piece * 2));
         }
       }
     };
-    auto widen = [&](uint8_t* dst) {
+    auto widen = [&](uint8_t* dst, const uint4 (&code)[kMine], const uint32_t (&scl)[kMine]) {
 #pragma unroll
       for (int i = 0; i < kMine; ++i) {
         const int flat = i * C::kWide + wt;
@@ -454,7 +476,12 @@ attn_many_kernel(AttnArgs a, int splits, int tiles_max) {
       }
       fence_proxy_async_smem();
     };
-    if (n > 0) load(js, 0);
+    if (n > 0) {
+      look_up(js);
+      load(js, 0, k_code, k_scl);
+      load(js, 1, v_code, v_scl);
+      look_up(js + 1);
+    }
     for (int i = 0; i < n; ++i) {
       const int st = i & 1;
       const uint32_t ph = (i >> 1) & 1;
@@ -463,20 +490,21 @@ attn_many_kernel(AttnArgs a, int splits, int tiles_max) {
         const int key = (js + i) * KVT + lane * 16;
         bool bad = false;
         if (lane < KVT / 16 && key < q.L) {
-          const int page = a.page_table[long(s) * a.max_pages + (key >> a.pool.shift)];
-          bad = page < 0 || page >= a.pool.n_pages;
+          const int p = __ldg(a.page_table + long(s) * a.max_pages + (key >> a.pool.shift));
+          bad = p < 0 || p >= a.pool.n_pages;
           if (bad) atomicExch(a.status, FRT_ERANGE);
         }
         const uint32_t mask = __ballot_sync(0xffffffffu, bad);
         if (lane == 0) k_hidden[i & 3] = mask;
       }
-      widen(k_s + st * C::kKvBytes);
+      widen(k_s + st * C::kKvBytes, k_code, k_scl);
       mbar_arrive(&k_full[st]);
-      load(js + i, 1);
+      if (i + 1 < n) load(js + i + 1, 0, k_code, k_scl);
       if (!wait_warp(&v_empty[st], ph ^ 1u)) break;
-      widen(v_s + st * C::kKvBytes);
+      widen(v_s + st * C::kKvBytes, v_code, v_scl);
       mbar_arrive(&v_full[st]);
-      if (i + 1 < n) load(js + i + 1, 0);
+      if (i + 1 < n) load(js + i + 1, 1, v_code, v_scl);
+      if (i + 2 < n) look_up(js + i + 2);
     }
   } else if (tid == 12 * 32) {
     // ------------------------------------------------------------ the MMAs ----
@@ -583,21 +611,23 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, int splits, 
   const int row = token * a.group + h - head * a.group;
   const long unit = (long(tiles_max - 1 - row / C::R) * a.n_seqs + s) * a.hkv + head;
   const int r = row % C::R;
-  float m = -INFINITY;
-  for (int i = 0; i < splits; ++i)
-    m = fmaxf(m, partial_tile<HD>(a.partials, unit * splits + i)[C::R * HD + r]);
-  float l = 0.0f, acc[V];
+  // lane i: the maximum, the sum and the weight of split i (16 at most)
+  const float* mine = partial_tile<HD>(a.partials, unit * splits + (lane < splits ? lane : 0));
+  const float mi = lane < splits ? mine[C::R * HD + r] : -INFINITY;
+  const float li = lane < splits ? mine[C::R * HD + C::R + r] : 0.0f;
+  const float m = warp_max(mi);
+  const float wi = mi == -INFINITY ? 0.0f : ex2(mi - m);  // 0: a share that the row does not see
+  const float l = warp_sum(wi * li);
+  float acc[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) acc[v] = 0.0f;
+#pragma unroll 4
   for (int i = 0; i < splits; ++i) {
-    const float* p = partial_tile<HD>(a.partials, unit * splits + i);
-    const float mi = p[C::R * HD + r];
-    if (mi == -INFINITY) continue;   // a share of the keys that the row does not see
-    const float f = ex2(mi - m);
-    l += p[C::R * HD + C::R + r] * f;
+    const float* p = partial_tile<HD>(a.partials, unit * splits + i) + long(r) * HD + lane * 2;
+    const float f = __shfl_sync(0xffffffffu, wi, i);
 #pragma unroll
     for (int v = 0; v < V; v += 2) {
-      const float2 x = *reinterpret_cast<const float2*>(p + long(r) * HD + (v / 2 * 32 + lane) * 2);
+      const float2 x = *reinterpret_cast<const float2*>(p + v * 32);
       acc[v] += x.x * f;
       acc[v + 1] += x.y * f;
     }
