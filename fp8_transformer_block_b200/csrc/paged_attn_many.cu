@@ -28,11 +28,19 @@ struct ManyCfg {
   static constexpr int KVT = HD == 256 ? 64 : 128; // keys of a tile
   static constexpr int R = 128 * QT;
   static constexpr int kWide = HD == 256 ? 256 : 128;  // threads that widen codes
-  static constexpr int kThreads = 32 * 13;         // 4 QT softmax warps, the widening, the MMAs
+  // four warpgroups: QT of softmax, the rest but one of widening, and the MMAs
+  static constexpr int kThreads = 512;
+  // registers a thread of each (setmaxnreg), of the launch's 512 x 128
+  static constexpr int kRegsSoftmax = QT == 2 ? 192 : 208;
+  static constexpr int kRegsWide = QT == 2 ? 88 : 128;
+  static constexpr int kRegsMma = 40;
+  static_assert(128 * (QT * kRegsSoftmax + (3 - QT) * kRegsWide + kRegsMma) <= 512 * 128,
+                "the shares exceed the launch's registers");
   static constexpr int kQBytes = 128 * HD * 2;     // one row tile
   static constexpr int kKvBytes = KVT * HD * 2;    // one K or V tile
   static constexpr int kBlock = KVT * 128;         // its 64-element column block
-  static constexpr int kSmem = QT * kQBytes + 4 * kKvBytes + 1024 + 256;
+  static constexpr int kCodeBytes = KVT * (HD / 2 + HD / 16);  // a tile's codes, then its scales
+  static constexpr int kSmem = QT * kQBytes + 4 * kKvBytes + 2 * kCodeBytes + 1024 + 256;
   // TMEM columns: two S (or P) slots, then O
   static constexpr int kTmem = 512;
   static constexpr int kO = 2 * KVT;
@@ -97,6 +105,24 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
       :: "memory");
 }
 
+__device__ __forceinline__ void pass_through(uint32_t (&r)[32]) {
+  asm volatile(""
+      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+        "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
+        "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]),
+        "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]),
+        "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
+}
+
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(N));
+}
+
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0],"
@@ -144,13 +170,16 @@ attn_many_kernel(AttnArgs a, int splits, int tiles_max) {
   uint8_t* q_s = smem;
   uint8_t* k_s = q_s + QT * C::kQBytes;
   uint8_t* v_s = k_s + 2 * C::kKvBytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(v_s + 2 * C::kKvBytes);
+  uint8_t* kc_s = v_s + 2 * C::kKvBytes;        // codes as they come from the pages
+  uint8_t* vc_s = kc_s + C::kCodeBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(vc_s + C::kCodeBytes);
   uint64_t *q_full = bars, *k_full = bars + 2, *k_empty = bars + 4, *v_full = bars + 6,
            *v_empty = bars + 8, *s_full = bars + 10, *p_full = bars + 12, *pv_done = bars + 14,
-           *done = bars + 16;
-  uint32_t* k_hidden = reinterpret_cast<uint32_t*>(bars + 17);  // [4] 16-key groups in bad pages
-  uint32_t* tmem_ptr = k_hidden + 4;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(k_hidden + 5);
+           *done = bars + 16, *kc_full = bars + 17, *kc_empty = bars + 18, *vc_full = bars + 19,
+           *vc_empty = bars + 20;
+  uint32_t* k_hidden = reinterpret_cast<uint32_t*>(bars + 21);  // [8] 16-key groups in bad pages
+  uint32_t* tmem_ptr = k_hidden + 8;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(k_hidden + 9);
 
   const int tid = int(threadIdx.x), warp = tid / 32, lane = tid % 32;
   pdl_trigger();
@@ -197,6 +226,10 @@ attn_many_kernel(AttnArgs a, int splits, int tiles_max) {
       mbar_init(&pv_done[i], 1);
     }
     mbar_init(done, 1);
+    mbar_init(kc_full, 1);
+    mbar_init(vc_full, 1);
+    mbar_init(kc_empty, C::kWide);
+    mbar_init(vc_empty, C::kWide);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -222,6 +255,7 @@ attn_many_kernel(AttnArgs a, int splits, int tiles_max) {
 
   if (warp < 4 * QT) {
     // ------------------------------------------------- softmax, one row ----
+    regs_inc<C::kRegsSoftmax>();
     const int t = warp / 4, r = tid % 128;
     const int row = tile * R + t * 128 + r;
     const bool live = row < q.Lq * a.group;
@@ -291,30 +325,33 @@ attn_many_kernel(AttnArgs a, int splits, int tiles_max) {
       if (!wait_warp(&s_full[slot], QT == 2 ? k & 1 : (k >> 1) & 1)) break;
       tc_fence_after();
       const uint32_t s_addr = lane_base + slot * KVT;
-      const uint32_t hidden = k_hidden[(j - js) & 3];
+      const uint32_t hidden = k_hidden[(j - js) & 7];
       const int key0 = j * KVT;
       const int rel_hi = lim_hi - key0, rel_lo = lim_lo - key0;
       const bool masked = __any_sync(0xffffffffu, rel_hi < KVT || rel_lo > 0) || hidden;
-      // drop what the row does not see from 32 scores
-      auto mask32 = [&](uint32_t (&x)[32], int base) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const bool out = base + i >= rel_hi || base + i < rel_lo || (hidden >> ((base + i) / 16) & 1);
-          if (out) x[i] = 0xFF800000u;  // -inf
-        }
-      };
-
-      // the row's largest product
+      // the row's products, all of them in registers, and the largest
+      uint32_t x[KVT / 32][32];
+      tmem_ld32_async(s_addr, x[0]);
+      tmem_ld32_async(s_addr + 32, x[1]);
       float mx = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < KVT / 32; ++i) {
-        uint32_t x[32];
-        tmem_ld32_async(s_addr + 32 * i, x);
-        tmem_wait_ld(x);
-        if (masked) mask32(x, 32 * i);
+      for (int i = 0; i < KVT / 32; i += 2) {
+        tmem_wait_ld(x[i]);
+        pass_through(x[i + 1]);
+        if (i + 2 < KVT / 32) {
+          tmem_ld32_async(s_addr + 32 * (i + 2), x[i + 2]);
+          tmem_ld32_async(s_addr + 32 * (i + 3), x[i + 3]);
+        }
+        if (masked) {  // drop what the row does not see
 #pragma unroll
-        for (int u = 0; u < 32; u += 2)
-          mx = fmaxf(fmaxf(mx, __uint_as_float(x[u])), __uint_as_float(x[u + 1]));
+          for (int u = 0; u < 64; ++u) {
+            const int at = 32 * i + u;
+            if (at >= rel_hi || at < rel_lo || (hidden >> (at / 16) & 1)) x[i + u / 32][u % 32] = 0xFF800000u;
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 64; u += 2)
+          mx = fmaxf(fmaxf(mx, __uint_as_float(x[i + u / 32][u % 32])), __uint_as_float(x[i + u / 32][u % 32 + 1]));
       }
       const float top = mx == -INFINITY ? mx : mx * c;
       // the maximum is raised only when a score passes it by more than 2^8
@@ -329,18 +366,18 @@ attn_many_kernel(AttnArgs a, int splits, int tiles_max) {
           // k wait for this warp: the parity names those of k - 1
           if (!wait_warp(&pv_done[t], (k - 1) & 1)) break;
           tc_fence_after();
-#pragma unroll
+#pragma unroll 1
           for (int i = 0; i < HD / 32; ++i) {
-            uint32_t x[32];
-            tmem_ld32_async(lane_base + C::kO + t * HD + 32 * i, x);
-            tmem_wait_ld(x);
+            uint32_t o[32];
+            tmem_ld32_async(lane_base + C::kO + t * HD + 32 * i, o);
+            tmem_wait_ld(o);
 #pragma unroll
-            for (int u = 0; u < 32; ++u) x[u] = __float_as_uint(__uint_as_float(x[u]) * f);
+            for (int u = 0; u < 32; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * f);
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
               uint32_t y[16];
 #pragma unroll
-              for (int w = 0; w < 16; ++w) y[w] = x[16 * u + w];
+              for (int w = 0; w < 16; ++w) y[w] = o[16 * u + w];
               tmem_st16(lane_base + C::kO + t * HD + 32 * i + 16 * u, y);
             }
           }
@@ -351,13 +388,10 @@ attn_many_kernel(AttnArgs a, int splits, int tiles_max) {
       const uint64_t base2 = f2_pack(base, base);
 #pragma unroll
       for (int i = 0; i < KVT / 32; ++i) {
-        uint32_t x[32], p[16];
-        tmem_ld32_async(s_addr + 32 * i, x);
-        tmem_wait_ld(x);
-        if (masked) mask32(x, 32 * i);
+        uint32_t p[16];
 #pragma unroll
         for (int u = 0; u < 16; ++u) {
-          const uint64_t v = fma2(f2_pack(__uint_as_float(x[2 * u]), __uint_as_float(x[2 * u + 1])), c2, base2);
+          const uint64_t v = fma2(f2_pack(__uint_as_float(x[i][2 * u]), __uint_as_float(x[i][2 * u + 1])), c2, base2);
           const float p0 = ex2(f2_lo(v)), p1 = ex2(f2_hi(v));
           l2 = add2(l2, f2_pack(p0, p1));
           p[u] = pack_f16x2(p0, p1);
@@ -412,45 +446,23 @@ attn_many_kernel(AttnArgs a, int splits, int tiles_max) {
     }
   } else if (warp < 12) {
     // ------------------------------------------- widening, K then V tiles ----
+    if constexpr (C::kRegsWide < 128) regs_dec<C::kRegsWide>();
     const int wt = tid - (12 * 32 - C::kWide);
     constexpr int kPieces = KVT * HD / 32;       // 32 codes and two scales
     constexpr int kMine = kPieces / C::kWide;
-    const int ps = a.pool.page_size;
-    // codes and scales of this thread's pieces of the next K and V tile, and
-    // the pages of the tile after it: no load is waited for where it is issued
-    uint4 k_code[kMine], v_code[kMine];
-    uint32_t k_scl[kMine], v_scl[kMine];
-    int page[kMine];
-    auto look_up = [&](int j) {
-#pragma unroll
-      for (int i = 0; i < kMine; ++i) {
-        const int key = j * KVT + (i * C::kWide + wt) / (HD / 32);
-        page[i] = key < q.L ? __ldg(a.page_table + long(s) * a.max_pages + (key >> a.pool.shift)) : -1;
-      }
-    };
-    auto load = [&](int j, int half, uint4 (&code)[kMine], uint32_t (&scl)[kMine]) {
-#pragma unroll
-      for (int i = 0; i < kMine; ++i) {
-        const int flat = i * C::kWide + wt;
-        const int at = (j * KVT + flat / (HD / 32)) & (ps - 1), piece = flat % (HD / 32);
-        code[i] = make_uint4(0, 0, 0, 0);
-        scl[i] = 0;
-        if (page[i] >= 0 && page[i] < a.pool.n_pages) {
-          const uint8_t* rec = a.pool.base + (long(page[i]) * a.pool.hkv + head) * a.pool.record_bytes +
-                               half * (a.pool.record_bytes / 2);
-          code[i] = __ldg(reinterpret_cast<const uint4*>(rec + at * (HD / 2) + piece * 16));
-          scl[i] = __ldg(reinterpret_cast<const uint16_t*>(rec + ps * (HD / 2) + at * (HD / 16) + piece * 2));
-        }
-      }
-    };
-    auto widen = [&](uint8_t* dst, const uint4 (&code)[kMine], const uint32_t (&scl)[kMine]) {
+    // one tile from its codes to fp16; a key behind the sequence's end or in a
+    // bad page comes out as zeros, whatever is there
+    auto widen = [&](uint8_t* dst, const uint8_t* src, int j, uint32_t hidden) {
 #pragma unroll
       for (int i = 0; i < kMine; ++i) {
         const int flat = i * C::kWide + wt;
         const int key = flat / (HD / 32), piece = flat % (HD / 32);
-        uint32_t sc = e4m3x2_to_f16(scl[i]);
+        const uint4 code = *reinterpret_cast<const uint4*>(src + flat * 16);
+        uint32_t sc = *reinterpret_cast<const uint16_t*>(src + KVT * (HD / 2) + flat * 2);
+        if (j * KVT + key >= q.L || (hidden >> (key / 16) & 1)) sc = 0;
+        sc = e4m3x2_to_f16(sc);
         uint8_t* rowp = dst + piece / 2 * C::kBlock + key * 128;
-        uint32_t w[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
+        uint32_t w[4] = {code.x, code.y, code.z, code.w};
         // eight neighbouring lanes write eight different 16-byte columns:
         // pieces of different column blocks start at different words
         const int turn = HD == 256 ? piece / 2 : HD == 128 ? piece / 2 * 2 : 0;
@@ -476,38 +488,23 @@ attn_many_kernel(AttnArgs a, int splits, int tiles_max) {
       }
       fence_proxy_async_smem();
     };
-    if (n > 0) {
-      look_up(js);
-      load(js, 0, k_code, k_scl);
-      load(js, 1, v_code, v_scl);
-      look_up(js + 1);
-    }
     for (int i = 0; i < n; ++i) {
       const int st = i & 1;
       const uint32_t ph = (i >> 1) & 1;
-      if (!wait_warp(&k_empty[st], ph ^ 1u)) break;
-      if (wt < 32) {  // one warp looks the tile's pages over for the mask
-        const int key = (js + i) * KVT + lane * 16;
-        bool bad = false;
-        if (lane < KVT / 16 && key < q.L) {
-          const int p = __ldg(a.page_table + long(s) * a.max_pages + (key >> a.pool.shift));
-          bad = p < 0 || p >= a.pool.n_pages;
-          if (bad) atomicExch(a.status, FRT_ERANGE);
-        }
-        const uint32_t mask = __ballot_sync(0xffffffffu, bad);
-        if (lane == 0) k_hidden[i & 3] = mask;
-      }
-      widen(k_s + st * C::kKvBytes, k_code, k_scl);
+      if (!wait_warp(kc_full, i & 1) || !wait_warp(&k_empty[st], ph ^ 1u)) break;
+      const uint32_t hidden = k_hidden[i & 7];
+      widen(k_s + st * C::kKvBytes, kc_s, js + i, hidden);
       mbar_arrive(&k_full[st]);
-      if (i + 1 < n) load(js + i + 1, 0, k_code, k_scl);
-      if (!wait_warp(&v_empty[st], ph ^ 1u)) break;
-      widen(v_s + st * C::kKvBytes, v_code, v_scl);
+      mbar_arrive(kc_empty);
+      if (!wait_warp(vc_full, i & 1) || !wait_warp(&v_empty[st], ph ^ 1u)) break;
+      widen(v_s + st * C::kKvBytes, vc_s, js + i, hidden);
       mbar_arrive(&v_full[st]);
-      if (i + 1 < n) load(js + i + 1, 1, v_code, v_scl);
-      if (i + 2 < n) look_up(js + i + 2);
+      mbar_arrive(vc_empty);
     }
-  } else if (tid == 12 * 32) {
+  } else {
     // ------------------------------------------------------------ the MMAs ----
+    regs_dec<C::kRegsMma>();
+    if (tid == 12 * 32) {
     constexpr uint32_t kQk = idesc_f16(128, KVT, false);
     constexpr uint32_t kPv = idesc_f16(128, HD, true);
     const uint32_t qa = smem_u32(q_s), ka = smem_u32(k_s), va = smem_u32(v_s);
@@ -584,6 +581,59 @@ attn_many_kernel(AttnArgs a, int splits, int tiles_max) {
     // nothing in flight when the tensor memory is freed
     umma_commit(done);
     mbar_wait_bounded(done, 0, kAttnWaitNs, nullptr);
+    } else if (warp == 13) {
+      // -------------------------------------------- the pages' codes, a tile ----
+      const int ps = a.pool.page_size;
+      const int span = min(ps, KVT), pieces = KVT / span;   // keys of a piece; lanes at work
+      auto look_up = [&](int j) {
+        const int key = j * KVT + lane * span;
+        if (lane >= pieces || key >= q.L) return -1;
+        return __ldg(a.page_table + long(s) * a.max_pages + (key >> a.pool.shift));
+      };
+      int next = n > 0 ? look_up(js) : -1;
+      bool ok = true;
+      int k_sent = 0, v_sent = 0;
+      for (int i = 0; ok && i < n; ++i) {
+        int page = next;
+        const int key = (js + i) * KVT + lane * span;
+        const bool bad = lane < pieces && key < q.L && (page < 0 || page >= a.pool.n_pages);
+        if (bad) {
+          atomicExch(a.status, FRT_ERANGE);
+          page = -1;
+        }
+        if (i + 1 < n) next = look_up(js + i + 1);
+        const uint32_t groups = ((1u << (span / 16)) - 1) << (lane * span / 16 & 31);
+        const uint32_t hidden = __reduce_or_sync(0xffffffffu, bad ? groups : 0u);
+        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, page >= 0)) * span * (HD / 2 + HD / 16);
+        const int at = key & (ps - 1);
+        for (int half = 0; ok && half < 2; ++half) {   // keys, values
+          uint64_t* full = half ? vc_full : kc_full;
+          if (lane == 0) {
+            ok = wait(half ? vc_empty : kc_empty, (i & 1) ^ 1u);
+            if (ok) {
+              if (!half) k_hidden[i & 7] = hidden;
+              mbar_arrive_expect_tx(full, bytes);
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) break;
+          (half ? v_sent : k_sent) = i + 1;
+          if (page >= 0) {
+            const uint8_t* rec = a.pool.base + (long(page) * a.pool.hkv + head) * a.pool.record_bytes +
+                                 half * (a.pool.record_bytes / 2);
+            uint8_t* dst = half ? vc_s : kc_s;
+            bulk_load(dst + lane * span * (HD / 2), rec + at * (HD / 2), span * (HD / 2), full);
+            bulk_load(dst + KVT * (HD / 2) + lane * span * (HD / 16),
+                      rec + ps * (HD / 2) + at * (HD / 16), span * (HD / 16), full);
+          }
+        }
+      }
+      // after a wait that ran out: no exit with copies in flight
+      if (*abort_flag && lane == 0) {
+        if (k_sent) mbar_wait_bounded(kc_full, (k_sent - 1) & 1, kAttnWaitNs, nullptr);
+        if (v_sent) mbar_wait_bounded(vc_full, (v_sent - 1) & 1, kAttnWaitNs, nullptr);
+      }
+    }
   }
   __syncwarp();
   tc_fence_before();
