@@ -31,16 +31,17 @@ struct ManyCfg {
   // four warpgroups: QT of softmax, the rest but one of widening, and the MMAs
   static constexpr int kThreads = 512;
   // registers a thread of each (setmaxnreg), of the launch's 512 x 128
-  static constexpr int kRegsSoftmax = QT == 2 ? 192 : 208;
-  static constexpr int kRegsWide = QT == 2 ? 88 : 128;
-  static constexpr int kRegsMma = 40;
+  static constexpr int kRegsSoftmax = QT == 2 ? 184 : 184;
+  static constexpr int kRegsWide = QT == 2 ? 80 : 128;
+  static constexpr int kRegsMma = QT == 2 ? 64 : 64;
   static_assert(128 * (QT * kRegsSoftmax + (3 - QT) * kRegsWide + kRegsMma) <= 512 * 128,
                 "the shares exceed the launch's registers");
   static constexpr int kQBytes = 128 * HD * 2;     // one row tile
   static constexpr int kKvBytes = KVT * HD * 2;    // one K or V tile
   static constexpr int kBlock = KVT * 128;         // its 64-element column block
   static constexpr int kCodeBytes = KVT * (HD / 2 + HD / 16);  // a tile's codes, then its scales
-  static constexpr int kSmem = QT * kQBytes + 4 * kKvBytes + 2 * kCodeBytes + 1024 + 256;
+  static constexpr int kRing = 3;                  // code tiles under way, keys and values in turn
+  static constexpr int kSmem = QT * kQBytes + 4 * kKvBytes + kRing * kCodeBytes + 1024 + 256;
   // TMEM columns: two S (or P) slots, then O
   static constexpr int kTmem = 512;
   static constexpr int kO = 2 * KVT;
@@ -114,13 +115,11 @@ __device__ __forceinline__ void pass_through(uint32_t (&r)[32]) {
         "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
 }
 
-template <int N>
-__device__ __forceinline__ void regs_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(N));
+// Every warp of a warpgroup moves its registers a thread up or down.
+template <int N, int FROM = 128>
+__device__ __forceinline__ void set_regs() {
+  if constexpr (N > FROM) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(N));
+  if constexpr (N < FROM) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(N));
 }
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -170,20 +169,46 @@ attn_many_kernel(AttnArgs a, int splits, int tiles_max) {
   uint8_t* q_s = smem;
   uint8_t* k_s = q_s + QT * C::kQBytes;
   uint8_t* v_s = k_s + 2 * C::kKvBytes;
-  uint8_t* kc_s = v_s + 2 * C::kKvBytes;        // codes as they come from the pages
-  uint8_t* vc_s = kc_s + C::kCodeBytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(vc_s + C::kCodeBytes);
-  uint64_t *q_full = bars, *k_full = bars + 2, *k_empty = bars + 4, *v_full = bars + 6,
+  // the rows of Q as they come, before there is a second K tile or a V tile
+  uint8_t* q_stage = k_s + C::kKvBytes;
+  static_assert(R * (HD * 2 + 16) <= 3 * C::kKvBytes, "Q does not fit its staging");
+  uint8_t* code_s = v_s + 2 * C::kKvBytes;      // codes as they come from the pages
+  uint64_t* bars = reinterpret_cast<uint64_t*>(code_s + C::kRing * C::kCodeBytes);
+  uint64_t *q_in = bars + 23, *q_full = bars, *k_full = bars + 2, *k_empty = bars + 4, *v_full = bars + 6,
            *v_empty = bars + 8, *s_full = bars + 10, *p_full = bars + 12, *pv_done = bars + 14,
-           *done = bars + 16, *kc_full = bars + 17, *kc_empty = bars + 18, *vc_full = bars + 19,
-           *vc_empty = bars + 20;
-  uint32_t* k_hidden = reinterpret_cast<uint32_t*>(bars + 21);  // [8] 16-key groups in bad pages
+           *done = bars + 16, *code_full = bars + 17, *code_empty = bars + 20;
+  uint32_t* k_hidden = reinterpret_cast<uint32_t*>(bars + 25);  // [8] 16-key groups in bad pages
   uint32_t* tmem_ptr = k_hidden + 8;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(k_hidden + 9);
 
   const int tid = int(threadIdx.x), warp = tid / 32, lane = tid % 32;
   pdl_trigger();
+  // what needs nothing of the kernel before
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_in[i], 4);
+      mbar_init(&q_full[i], 128);
+      mbar_init(&k_full[i], C::kWide);
+      mbar_init(&v_full[i], C::kWide);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_empty[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 128);
+      mbar_init(&pv_done[i], 1);
+    }
+    mbar_init(done, 1);
+    for (int i = 0; i < C::kRing; ++i) {
+      mbar_init(&code_full[i], 1);
+      mbar_init(&code_empty[i], C::kWide);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
   pdl_wait();
+  if (warp == 12) {
+    tmem_alloc(tmem_ptr, C::kTmem);
+    tmem_relinquish();
+  }
   long b = blockIdx.x;
   const long part_index = b;
   const int split = int(b % splits);
@@ -194,7 +219,7 @@ attn_many_kernel(AttnArgs a, int splits, int tiles_max) {
   // causal tiles with the most keys first
   const int tile = tiles_max - 1 - int(b / a.n_seqs);
   const Seq q = load_seq<R, KVT>(a, s, tile == 0 && head == 0 && split == 0 && tid == 0);
-  if (tile >= q.tiles) return;
+  const bool any_rows = tile < q.tiles;
 
   int begin[QT], end[QT], lo = 0x7fffffff, hi = 0;
 #pragma unroll
@@ -213,34 +238,14 @@ attn_many_kernel(AttnArgs a, int splits, int tiles_max) {
     end[t] = min(end[t], je);
   }
   const int n = n_all ? je - js : 0;
-
-  if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&q_full[i], 128);
-      mbar_init(&k_full[i], C::kWide);
-      mbar_init(&v_full[i], C::kWide);
-      mbar_init(&k_empty[i], 1);
-      mbar_init(&v_empty[i], 1);
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 128);
-      mbar_init(&pv_done[i], 1);
-    }
-    mbar_init(done, 1);
-    mbar_init(kc_full, 1);
-    mbar_init(vc_full, 1);
-    mbar_init(kc_empty, C::kWide);
-    mbar_init(vc_empty, C::kWide);
-    *abort_flag = 0;
-    fence_barrier_init();
-  }
-  if (warp == 12) {
-    tmem_alloc(tmem_ptr, C::kTmem);
-    tmem_relinquish();
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_ptr;
+  if (!any_rows) {
+    if (warp == 12) tmem_dealloc(tmem, C::kTmem);
+    return;
+  }
 
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (mbar_wait_bounded(bar, parity, kAttnWaitNs, abort_flag)) return true;
@@ -255,57 +260,46 @@ attn_many_kernel(AttnArgs a, int splits, int tiles_max) {
 
   if (warp < 4 * QT) {
     // ------------------------------------------------- softmax, one row ----
-    regs_inc<C::kRegsSoftmax>();
+    set_regs<C::kRegsSoftmax>();
     const int t = warp / 4, r = tid % 128;
     const int row = tile * R + t * 128 + r;
     const bool live = row < q.Lq * a.group;
     const int token = live ? row / a.group : 0;
     const int h = head * a.group + (live ? row - token * a.group : 0);
+    const int n_live = max(0, min(32, q.Lq * a.group - (row - lane)));  // of this warp
     const uint32_t lane_base = tmem + (uint32_t(warp % 4 * 32) << 16);
 
-    // Q: fp16 under a power of two that brings the row's largest below 2.
-    // HD / 8 lanes read a row (16 bytes each), 4 batches of 8 warp loads.
+    // Q: a bulk copy of each row (padded, so that the threads' rows start at
+    // different banks) into what will be K and V buffers, then fp16 under a
+    // power of two that brings the row's largest below 2
     const float scale = *a.k_scale * a.sm_scale * kLog2e;
-    constexpr int kLanes = HD / 8, kRows = 32 / kLanes;   // rows of a warp load
-    constexpr int kBatch = HD == 256 ? 16 : HD == 128 ? 16 : 8;
-    float c = 0.0f;
-#pragma unroll 1
-    for (int base = 0; base < 32 / kRows; base += kBatch) {
-      uint4 raw[kBatch];
+    uint8_t* in = q_stage + (t * 128 + r) * (HD * 2 + 16);
+    if (lane == 0) mbar_arrive_expect_tx(&q_in[t], n_live * HD * 2);
+    __syncwarp();
+    if (live) bulk_load(in, a.q + long(q.r0 + token) * a.ld_q + long(h) * HD, HD * 2, &q_in[t]);
+    const bool got_q = wait_warp(&q_in[t], 0);
+    if (!got_q) mbar_wait_bounded(&q_in[t], 0, kAttnWaitNs, nullptr);  // no exit with copies in flight
+    float big = 0.0f;
+#pragma unroll 4
+    for (int i = 0; i < HD / 8; ++i) {
+      float f[8];
+      unpack8(*reinterpret_cast<const uint4*>(in + i * 16), f);
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int x = tile * R + t * 128 + warp % 4 * 32 + (base + i) * kRows + lane / kLanes;
-        const int tok = x / a.group;
-        raw[i] = make_uint4(0, 0, 0, 0);
-        if (x < q.Lq * a.group)
-          raw[i] = *reinterpret_cast<const uint4*>(a.q + long(q.r0 + tok) * a.ld_q +
-                                                   long(head * a.group + x - tok * a.group) * HD +
-                                                   lane % kLanes * 8);
-      }
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        float f[8], big = 0.0f;
-        unpack8(raw[i], f);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) big = fmaxf(big, fabsf(f[k]));
-#pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-        int e = int(__float_as_uint(big) >> 23);
-        if (e < 1 || e > 253) e = 127;
-        // the sign of the scale goes into Q, so that the largest score is that
-        // of the largest product
-        const float down = copysignf(__uint_as_float(uint32_t(254 - e) << 23), scale);
-        const int rr = warp % 4 * 32 + (base + i) * kRows + lane / kLanes, col = lane % kLanes;
-        *reinterpret_cast<uint4*>(q_s + t * C::kQBytes + col / 8 * (128 * 128) + rr * 128 +
-                                  ((col % 8) ^ (rr & 7)) * 16) =
-            make_uint4(pack_f16x2(f[0] * down, f[1] * down), pack_f16x2(f[2] * down, f[3] * down),
-                       pack_f16x2(f[4] * down, f[5] * down), pack_f16x2(f[6] * down, f[7] * down));
-        // the row's own thread keeps its factor
-        const float up = __uint_as_float(uint32_t(e) << 23);
-        const int own = lane - (base + i) * kRows;
-        const float theirs = __shfl_sync(0xffffffffu, up, own >= 0 && own < kRows ? own * kLanes : 0);
-        if (own >= 0 && own < kRows) c = theirs * (scale == 0.0f ? kTinyScale : fabsf(scale));
-      }
+      for (int k = 0; k < 8; ++k) big = fmaxf(big, fabsf(f[k]));
+    }
+    int e = int(__float_as_uint(big) >> 23);
+    if (e < 1 || e > 253) e = 127;
+    // the sign of the scale goes into Q, so that the largest score is that of
+    // the largest product
+    const float down = copysignf(__uint_as_float(uint32_t(254 - e) << 23), scale);
+    const float c = (scale == 0.0f ? kTinyScale : fabsf(scale)) * __uint_as_float(uint32_t(e) << 23);
+#pragma unroll 4
+    for (int i = 0; i < HD / 8; ++i) {
+      float f[8];
+      unpack8(*reinterpret_cast<const uint4*>(in + i * 16), f);
+      *reinterpret_cast<uint4*>(q_s + t * C::kQBytes + i / 8 * (128 * 128) + r * 128 + ((i % 8) ^ (r & 7)) * 16) =
+          make_uint4(pack_f16x2(f[0] * down, f[1] * down), pack_f16x2(f[2] * down, f[3] * down),
+                     pack_f16x2(f[4] * down, f[5] * down), pack_f16x2(f[6] * down, f[7] * down));
     }
     fence_proxy_async_smem();
     mbar_arrive(&q_full[t]);
@@ -320,7 +314,7 @@ attn_many_kernel(AttnArgs a, int splits, int tiles_max) {
     uint64_t l2 = 0;
     int k = 0;
     const uint64_t c2 = f2_pack(c, c);
-    for (int j = begin[t]; j < end[t]; ++j, ++k) {
+    for (int j = begin[t]; got_q && j < end[t]; ++j, ++k) {
       const int slot = QT == 2 ? t : k & 1;
       if (!wait_warp(&s_full[slot], QT == 2 ? k & 1 : (k >> 1) & 1)) break;
       tc_fence_after();
@@ -329,7 +323,18 @@ attn_many_kernel(AttnArgs a, int splits, int tiles_max) {
       const int key0 = j * KVT;
       const int rel_hi = lim_hi - key0, rel_lo = lim_lo - key0;
       const bool masked = __any_sync(0xffffffffu, rel_hi < KVT || rel_lo > 0) || hidden;
-      // the row's products, all of them in registers, and the largest
+      // drop what the row does not see from 32 products
+      auto mask32 = [&](uint32_t (&x)[32], int base) {
+#pragma unroll
+        for (int u = 0; u < 32; ++u)
+          if (base + u >= rel_hi || base + u < rel_lo || (hidden >> ((base + u) / 16) & 1)) x[u] = 0xFF800000u;
+      };
+      auto max32 = [](const uint32_t (&x)[32], float v) {
+#pragma unroll
+        for (int u = 0; u < 32; u += 2)
+          v = fmaxf(fmaxf(v, __uint_as_float(x[u])), __uint_as_float(x[u + 1]));
+        return v;
+      };
       uint32_t x[KVT / 32][32];
       tmem_ld32_async(s_addr, x[0]);
       tmem_ld32_async(s_addr + 32, x[1]);
@@ -342,16 +347,11 @@ attn_many_kernel(AttnArgs a, int splits, int tiles_max) {
           tmem_ld32_async(s_addr + 32 * (i + 2), x[i + 2]);
           tmem_ld32_async(s_addr + 32 * (i + 3), x[i + 3]);
         }
-        if (masked) {  // drop what the row does not see
-#pragma unroll
-          for (int u = 0; u < 64; ++u) {
-            const int at = 32 * i + u;
-            if (at >= rel_hi || at < rel_lo || (hidden >> (at / 16) & 1)) x[i + u / 32][u % 32] = 0xFF800000u;
-          }
+        if (masked) {
+          mask32(x[i], 32 * i);
+          mask32(x[i + 1], 32 * i + 32);
         }
-#pragma unroll
-        for (int u = 0; u < 64; u += 2)
-          mx = fmaxf(fmaxf(mx, __uint_as_float(x[i + u / 32][u % 32])), __uint_as_float(x[i + u / 32][u % 32 + 1]));
+        mx = max32(x[i + 1], max32(x[i], mx));
       }
       const float top = mx == -INFINITY ? mx : mx * c;
       // the maximum is raised only when a score passes it by more than 2^8
@@ -386,57 +386,74 @@ attn_many_kernel(AttnArgs a, int splits, int tiles_max) {
       }
       const float base = m == -INFINITY ? 0.0f : -m;
       const uint64_t base2 = f2_pack(base, base);
-#pragma unroll
-      for (int i = 0; i < KVT / 32; ++i) {
+      auto weigh32 = [&](const uint32_t (&x)[32], int i) {
         uint32_t p[16];
 #pragma unroll
         for (int u = 0; u < 16; ++u) {
-          const uint64_t v = fma2(f2_pack(__uint_as_float(x[i][2 * u]), __uint_as_float(x[i][2 * u + 1])), c2, base2);
+          const uint64_t v = fma2(f2_pack(__uint_as_float(x[2 * u]), __uint_as_float(x[2 * u + 1])), c2, base2);
           const float p0 = ex2(f2_lo(v)), p1 = ex2(f2_hi(v));
           l2 = add2(l2, f2_pack(p0, p1));
           p[u] = pack_f16x2(p0, p1);
         }
         tmem_st16(s_addr + 16 * i, p);
-      }
+      };
+#pragma unroll
+      for (int i = 0; i < KVT / 32; ++i) weigh32(x[i], i);
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(&p_full[slot]);
     }
 
-    // --- the row's result ---
+    // --- the row's result: through shared memory (every buffer is idle
+    // now), so that the stores are whole rows ---
     const float l = f2_lo(l2) + f2_hi(l2);
     const bool whole = splits == 1;
     float* part = partial_tile<HD>(a.partials, part_index);
     const float inv = l > 0.0f ? *a.v_scale / l : l * *a.v_scale;
-    if (k > 0 && !wait_warp(done, 0)) k = 0;  // every product issued is in
+    if (!wait_warp(done, 0)) k = 0;  // every product of the CTA is in
     tc_fence_after();
+    const int row_bytes = whole ? HD * 2 : HD * 4;
+    const int stride = row_bytes + 16;
+    uint8_t* staged = smem + (t * 128 + warp % 4 * 32) * (HD * 4 + 16);
+    uint8_t* mine = staged + lane * stride;
 #pragma unroll 1
     for (int i = 0; i < HD / 32; ++i) {
       uint32_t x[32];
-      if (k > 0) {
-        tmem_ld32_async(lane_base + C::kO + t * HD + 32 * i, x);
-        tmem_wait_ld(x);
-      } else {
+      tmem_ld32_async(lane_base + C::kO + t * HD + 32 * i, x);
+      tmem_wait_ld(x);
+      if (k == 0) {  // nothing was summed
 #pragma unroll
         for (int u = 0; u < 32; ++u) x[u] = 0;
       }
-      if (live && whole) {
-        uint4* dst = reinterpret_cast<uint4*>(a.out + long(q.r0 + token) * a.ld_out + long(h) * HD + 32 * i);
+      if (whole) {
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           float f[8];
 #pragma unroll
           for (int w = 0; w < 8; ++w) f[w] = __uint_as_float(x[8 * u + w]) * inv;
-          dst[u] = pack8_bf16(f);
+          *reinterpret_cast<uint4*>(mine + i * 64 + u * 16) = pack8_bf16(f);
         }
-      } else if (live) {
-        float4* dst = reinterpret_cast<float4*>(part + long(t * 128 + r) * HD + 32 * i);
+      } else {
 #pragma unroll
         for (int u = 0; u < 8; ++u)
-          dst[u] = make_float4(__uint_as_float(x[4 * u]), __uint_as_float(x[4 * u + 1]),
-                               __uint_as_float(x[4 * u + 2]), __uint_as_float(x[4 * u + 3]));
+          *reinterpret_cast<uint4*>(mine + i * 128 + u * 16) =
+              make_uint4(x[4 * u], x[4 * u + 1], x[4 * u + 2], x[4 * u + 3]);
       }
-      __syncwarp();
+    }
+    uint8_t* dst = whole ? reinterpret_cast<uint8_t*>(a.out + long(q.r0 + token) * a.ld_out + long(h) * HD)
+                         : reinterpret_cast<uint8_t*>(part + long(t * 128 + r) * HD);
+    __syncwarp();
+    constexpr int kShift = HD == 64 ? 3 : HD == 128 ? 4 : 5;   // 16-byte pieces of a bf16 row
+    const int shift = whole ? kShift : kShift + 1;
+    for (int base = 0; base < n_live << shift; base += 32 * 4) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int x = base + 32 * u + lane, rr = x >> shift, at = (x & ((1 << shift) - 1)) * 16;
+        uint8_t* to = reinterpret_cast<uint8_t*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), rr & 31));
+        if (rr < n_live)
+          *reinterpret_cast<uint4*>(to + at) = *reinterpret_cast<const uint4*>(staged + rr * stride + at);
+      }
     }
     if (live && whole && a.lse)
       a.lse[long(q.r0 + token) * a.hq + h] = m == -INFINITY ? m : (m + log2f(l)) * kLn2;
@@ -446,7 +463,7 @@ attn_many_kernel(AttnArgs a, int splits, int tiles_max) {
     }
   } else if (warp < 12) {
     // ------------------------------------------- widening, K then V tiles ----
-    if constexpr (C::kRegsWide < 128) regs_dec<C::kRegsWide>();
+    set_regs<C::kRegsWide>();
     const int wt = tid - (12 * 32 - C::kWide);
     constexpr int kPieces = KVT * HD / 32;       // 32 codes and two scales
     constexpr int kMine = kPieces / C::kWide;
@@ -488,22 +505,27 @@ attn_many_kernel(AttnArgs a, int splits, int tiles_max) {
       }
       fence_proxy_async_smem();
     };
-    for (int i = 0; i < n; ++i) {
-      const int st = i & 1;
-      const uint32_t ph = (i >> 1) & 1;
-      if (!wait_warp(kc_full, i & 1) || !wait_warp(&k_empty[st], ph ^ 1u)) break;
-      const uint32_t hidden = k_hidden[i & 7];
-      widen(k_s + st * C::kKvBytes, kc_s, js + i, hidden);
-      mbar_arrive(&k_full[st]);
-      mbar_arrive(kc_empty);
-      if (!wait_warp(vc_full, i & 1) || !wait_warp(&v_empty[st], ph ^ 1u)) break;
-      widen(v_s + st * C::kKvBytes, vc_s, js + i, hidden);
-      mbar_arrive(&v_full[st]);
-      mbar_arrive(vc_empty);
+    int slot = 0;
+    uint32_t turn = 0;
+    for (int i = 0; i < 2 * n; ++i) {        // keys and values of tile i / 2
+      const int st = i >> 1 & 1;
+      const uint32_t ph = i >> 2 & 1;
+      const bool v = i & 1;
+      if (!wait_warp(&code_full[slot], turn) || !wait_warp(v ? &v_empty[st] : &k_empty[st], ph ^ 1u)) break;
+      if (i == 1) {   // from here on, over Q's staging
+        bool ok = true;
+        for (int t = 0; t < QT; ++t) ok = ok && wait_warp(&q_full[t], 0);
+        if (!ok) break;
+      }
+      widen((v ? v_s : k_s) + st * C::kKvBytes, code_s + slot * C::kCodeBytes, js + i / 2,
+            k_hidden[i / 2 & 7]);
+      mbar_arrive(v ? &v_full[st] : &k_full[st]);
+      mbar_arrive(&code_empty[slot]);
+      if (++slot == C::kRing) { slot = 0; turn ^= 1u; }
     }
   } else {
     // ------------------------------------------------------------ the MMAs ----
-    regs_dec<C::kRegsMma>();
+    set_regs<C::kRegsMma>();
     if (tid == 12 * 32) {
     constexpr uint32_t kQk = idesc_f16(128, KVT, false);
     constexpr uint32_t kPv = idesc_f16(128, HD, true);
@@ -592,7 +614,8 @@ attn_many_kernel(AttnArgs a, int splits, int tiles_max) {
       };
       int next = n > 0 ? look_up(js) : -1;
       bool ok = true;
-      int k_sent = 0, v_sent = 0;
+      int slot = 0, sent = 0;
+      uint32_t turn = 0;
       for (int i = 0; ok && i < n; ++i) {
         int page = next;
         const int key = (js + i) * KVT + lane * span;
@@ -607,32 +630,31 @@ attn_many_kernel(AttnArgs a, int splits, int tiles_max) {
         const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, page >= 0)) * span * (HD / 2 + HD / 16);
         const int at = key & (ps - 1);
         for (int half = 0; ok && half < 2; ++half) {   // keys, values
-          uint64_t* full = half ? vc_full : kc_full;
           if (lane == 0) {
-            ok = wait(half ? vc_empty : kc_empty, (i & 1) ^ 1u);
+            ok = wait(&code_empty[slot], turn ^ 1u);
             if (ok) {
               if (!half) k_hidden[i & 7] = hidden;
-              mbar_arrive_expect_tx(full, bytes);
+              mbar_arrive_expect_tx(&code_full[slot], bytes);
             }
           }
           ok = __shfl_sync(0xffffffffu, ok, 0);
           if (!ok) break;
-          (half ? v_sent : k_sent) = i + 1;
+          ++sent;
           if (page >= 0) {
             const uint8_t* rec = a.pool.base + (long(page) * a.pool.hkv + head) * a.pool.record_bytes +
                                  half * (a.pool.record_bytes / 2);
-            uint8_t* dst = half ? vc_s : kc_s;
-            bulk_load(dst + lane * span * (HD / 2), rec + at * (HD / 2), span * (HD / 2), full);
+            uint8_t* dst = code_s + slot * C::kCodeBytes;
+            bulk_load(dst + lane * span * (HD / 2), rec + at * (HD / 2), span * (HD / 2), &code_full[slot]);
             bulk_load(dst + KVT * (HD / 2) + lane * span * (HD / 16),
-                      rec + ps * (HD / 2) + at * (HD / 16), span * (HD / 16), full);
+                      rec + ps * (HD / 2) + at * (HD / 16), span * (HD / 16), &code_full[slot]);
           }
+          if (++slot == C::kRing) { slot = 0; turn ^= 1u; }
         }
       }
       // after a wait that ran out: no exit with copies in flight
-      if (*abort_flag && lane == 0) {
-        if (k_sent) mbar_wait_bounded(kc_full, (k_sent - 1) & 1, kAttnWaitNs, nullptr);
-        if (v_sent) mbar_wait_bounded(vc_full, (v_sent - 1) & 1, kAttnWaitNs, nullptr);
-      }
+      if (*abort_flag && lane == 0)
+        for (int i = max(0, sent - C::kRing); i < sent; ++i)
+          mbar_wait_bounded(&code_full[i % C::kRing], i / C::kRing & 1, kAttnWaitNs, nullptr);
     }
   }
   __syncwarp();
@@ -710,10 +732,10 @@ struct Many {
   static int launch(AttnArgs a, void* ws, cudaStream_t st) {
     auto kern = attn_many_kernel<HD>;
     if (int rc = allow_smem(reinterpret_cast<const void*>(kern), C::kSmem)) return rc;
-    // two key tiles a split at least
-    const long key_tiles = (long(a.max_pages) * a.pool.page_size + C::KVT - 1) / C::KVT;
+    // 128 keys a split at least: with fewer, joining costs what it saves
+    const long most = (long(a.max_pages) * a.pool.page_size + 127) / 128;
     int n = splits(a.n_seqs, a.max_q, a.hq, a.hkv);
-    if (n > 1 && n > key_tiles / 2) n = key_tiles < 2 ? 1 : int(key_tiles / 2);
+    if (n > most) n = most < 1 ? 1 : int(most);
     a.partials = static_cast<float*>(ws);
     const int tm = int(tiles(a.max_q, a.group));
     const long blocks = units(a.n_seqs, a.max_q, a.hq, a.hkv) * n;
