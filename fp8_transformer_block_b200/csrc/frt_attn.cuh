@@ -16,6 +16,11 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kTinyScale = 1e-30f;
 // the running maximum of a row that has seen no key
 constexpr float kNoKey = -1e30f;
+// Weights are 2^(score - m) and go to the tensor cores in fp16.  m is set to
+// the largest score so far less kLift, and again once a score passes m by
+// kGrow: weights stay below 2^15, and those down to 2^-21 of the largest keep
+// all eleven bits (the least step is 2^-31 of it).
+constexpr float kLift = 7.0f, kGrow = 15.0f;
 
 struct AttnArgs {
   int n_seqs, rows, max_q, hq, hkv, group, causal, window;

@@ -142,7 +142,8 @@ attn_few_kernel(AttnArgs a) {
   long* scan = reinterpret_cast<long*>(valid + 8);    // [kThreads / 32] and the start
   volatile int* abort_flag = reinterpret_cast<volatile int*>(scan + 8);
   int* last = reinterpret_cast<int*>(scan + 8) + 1;
-  Seq* start = reinterpret_cast<Seq*>(scan + 9);
+  int* units = reinterpret_cast<int*>(scan + 9);
+  Seq* start = reinterpret_cast<Seq*>(scan + 10);
 
   const int tid = int(threadIdx.x), warp = tid / 32, lane = tid % 32;
   pdl_trigger();
@@ -152,6 +153,7 @@ attn_few_kernel(AttnArgs a) {
       mbar_init(&empty[i], W);
     }
     *abort_flag = 0;
+    *units = 0;
     fence_barrier_init();
   }
   __syncthreads();
@@ -167,6 +169,7 @@ attn_few_kernel(AttnArgs a) {
     if (s < a.n_seqs) {
       mine = load_seq<R, CK>(a, s, blockIdx.x == 0);
       n = mine.work(a.hkv);
+      if (mine.tiles) atomicAdd(units, mine.tiles * a.hkv);
     }
     long inc = n;
 #pragma unroll
@@ -185,8 +188,14 @@ attn_few_kernel(AttnArgs a) {
     total += all;
     __syncthreads();
   }
-  // no more CTAs than chunks
-  const long ctas = total < long(gridDim.x) ? total : long(gridDim.x);
+  // A chunk takes a CTA about a microsecond, and joining a unit's shares an
+  // eighth of one a share and eight rows: of a unit's n chunks, sqrt(n NT / 8)
+  // to a CTA keep the sum of both low (one sequence of 40000 keys: 48 us with
+  // a CTA for every chunk, 24 us with this)
+  const float mean = float(total) / float(max(*units, 1));
+  const long least = max(1L, long(sqrtf(mean * NT / 8) + 0.5f));
+  const long most = (total + least - 1) / least;
+  const long ctas = most < long(gridDim.x) ? most : long(gridDim.x);
   const long c = blockIdx.x;
   if (c >= ctas) return;
   const long begin = c * total / ctas, end = (c + 1) * total / ctas;
@@ -510,9 +519,10 @@ attn_few_kernel(AttnArgs a) {
           }
         }
 
-        // softmax: base-2 scores against a running maximum that is raised
-        // only when a score passes it by more than 2^8 (the weights then
-        // stay within fp16), so most groups pass without the reduction
+        // softmax: base-2 scores against a running maximum (kLift below the
+        // largest score when it is set) that is raised only when a score
+        // passes it by more than kGrow, so most groups pass without the
+        // reduction
         if (masked) {
 #pragma unroll
           for (int u = 0; u < GR; ++u)
@@ -535,7 +545,7 @@ attn_few_kernel(AttnArgs a) {
 #pragma unroll
             for (int u = 1; u < GR; ++u) v = fmaxf(v, fmaxf(s[u][nt][e2], s[u][nt][e2 + 2]));
             top[nt][e2] = v * cq[nt][e2];
-            grow |= top[nt][e2] > m[nt][e2] + 8.0f;
+            grow |= top[nt][e2] > m[nt][e2] + kGrow;
           }
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -545,7 +555,7 @@ attn_few_kernel(AttnArgs a) {
               float v = top[nt][e2];
 #pragma unroll
               for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-              v = fmaxf(v, m[nt][e2]);
+              v = fmaxf(v - kLift, m[nt][e2]);
               const float f = ex2(m[nt][e2] - v);
               m[nt][e2] = v;
               l[nt][e2] *= f;
@@ -698,29 +708,70 @@ attn_few_kernel(AttnArgs a) {
       named_bar_sync(1, W * 32);
       if (*last) {
         __threadfence();
-        for (int i = tid; i < R * (HD / 4); i += W * 32) {
-          const int r = i / (HD / 4), d = i % (HD / 4) * 4;
+        // the shares' maxima first, a lane each; then their weights (as many
+        // at a time as the idle join buffer holds), then the sums with every
+        // share's loads under way
+        constexpr int kCap = W * HD / 2;
+        const int shares = int(final - first) + 1;
+        auto share = [&](int k) { return a.partials + (2 * (first + k) + (k == 0)) * C::kTile; };
+        // one pass for up to 32 shares; code that runs once is fetched cold,
+        // so what follows is kept in loops
+#pragma unroll 1
+        for (int r = warp; r < R; r += W) {
+          float mm = kNoKey, ll = 0.0f;
+#pragma unroll 1
+          for (int k = lane; k < shares; k += 32) {
+            const float* pt = share(k) + R * HD + r;
+            const float mk = __ldcg(pt), lk = __ldcg(pt + R);
+            const float top = fmaxf(mm, mk);
+            ll = ll * ex2(mm - top) + lk * ex2(mk - top);
+            mm = top;
+          }
+          const float top = warp_max(mm);
+          ll = warp_sum(ll * ex2(mm - top));
+          if (lane == 0) {
+            join_m[r] = top;
+            join_l[r] = ll;
+          }
+        }
+        constexpr int kItems = R * (HD / 4) / (W * 32);
+        float4 acc[kItems];
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) acc[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int k0 = 0; k0 < shares; k0 += kCap) {
+          const int kn = min(kCap, shares - k0);
+          named_bar_sync(1, W * 32);   // join_m; the block before
+          for (int i = tid; i < R * kn; i += W * 32) {
+            const int r = i % R, k = i / R;
+            join[r * kCap + k] = ex2(__ldcg(share(k0 + k) + R * HD + r) - join_m[r]);
+          }
+          named_bar_sync(1, W * 32);
+#pragma unroll 4
+          for (int k = 0; k < kn; ++k) {
+            const float* pt = share(k0 + k);
+#pragma unroll
+            for (int i = 0; i < kItems; ++i) {
+              const int item = i * W * 32 + tid, r = item / (HD / 4);
+              const float f = join[r * kCap + k];
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(pt + r * HD + item % (HD / 4) * 4));
+              acc[i].x += v.x * f; acc[i].y += v.y * f; acc[i].z += v.z * f; acc[i].w += v.w * f;
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+          const int item = i * W * 32 + tid, r = item / (HD / 4), d = item % (HD / 4) * 4;
           const int row = tile * R + r;
           if (row >= rows_here) continue;
-          float mm = kNoKey, ll = 0.0f;
-          for (long k = first; k <= final; ++k)
-            mm = fmaxf(mm, __ldcg(a.partials + (2 * k + (k == first)) * C::kTile + R * HD + r));
-          float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-          for (long k = first; k <= final; ++k) {
-            const float* pt = a.partials + (2 * k + (k == first)) * C::kTile;
-            const float f = ex2(__ldcg(pt + R * HD + r) - mm);
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(pt + r * HD + d));
-            ll += __ldcg(pt + R * HD + R + r) * f;
-            acc.x += v.x * f; acc.y += v.y * f; acc.z += v.z * f; acc.w += v.w * f;
-          }
           const int token = row / a.group, h = head * a.group + row - token * a.group;
+          const float ll = join_l[r];
           const float inv = ll > 0.0f ? vscale / ll : ll * vscale;
           *reinterpret_cast<uint2*>(a.out + long(w.q.r0 + token) * a.ld_out + long(h) * HD + d) =
-              make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv),
-                         pack_bf16x2(acc.z * inv, acc.w * inv));
+              make_uint2(pack_bf16x2(acc[i].x * inv, acc[i].y * inv),
+                         pack_bf16x2(acc[i].z * inv, acc[i].w * inv));
           if (d == 0 && a.lse)
-            a.lse[long(w.q.r0 + token) * a.hq + h] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+            a.lse[long(w.q.r0 + token) * a.hq + h] =
+                ll == 0.0f ? -INFINITY : (join_m[r] + log2f(ll)) * kLn2;
         }
       }
     }
@@ -731,19 +782,21 @@ attn_few_kernel(AttnArgs a) {
 
 // ---------------------------------------------------------------- launch --
 
+// Counters of the cut units, at the head of the workspace: no kernel leaves
+// anything else there.
+constexpr size_t kCounterBytes = 4096;
+
 template <int HD, int NT>
 struct Few {
   using C = FewCfg<HD, NT>;
   static int grid() { return num_sms() * C::kCtas; }
-  static size_t workspace() {
-    return (size_t(grid()) * 4 + 255) / 256 * 256 + size_t(grid()) * 2 * C::kTile * 4;
-  }
+  static size_t workspace() { return kCounterBytes + size_t(grid()) * 2 * C::kTile * 4; }
   static int launch(AttnArgs a, void* ws, long most_chunks, cudaStream_t s) {
+    FRT_REQUIRE(size_t(grid()) * 4 <= kCounterBytes, FRT_ECUDA, "more SMs than counters");
     auto kern = attn_few_kernel<HD, NT>;
     if (int rc = allow_smem(reinterpret_cast<const void*>(kern), C::kSmem)) return rc;
     a.counters = static_cast<int*>(ws);
-    a.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) +
-                                          (size_t(grid()) * 4 + 255) / 256 * 256);
+    a.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kCounterBytes);
     const int n = most_chunks < grid() ? int(most_chunks) : grid();
     return launch_pdl("frt_paged_attention_fp4", kern, dim3(n), dim3(C::kThreads), C::kSmem, s, a);
   }
@@ -759,8 +812,18 @@ auto with_variant(int hd, long rows_per_head, F f) {
   return rows_per_head <= 8 ? f(Few<256, 1>{}) : f(Few<256, 2>{});
 }
 
-// Rows of one kv head from which the tensor-memory kernel takes over.
-bool many_rows(long rows_per_head) { return rows_per_head > 32; }
+// Which kernel takes the rows of one kv head.  Above 32 rows always the
+// tensor-memory one.  For 9 to 32 rows the register kernel streams the cache
+// faster (32 sequences of 700 to 8000 keys, 16 rows: 37 us against 110), but
+// where the units are few and the table short, the other's splits are done
+// sooner (3 sequences of 900 to 2000 keys, 2 kv heads: 16 rows 16.6 us
+// against 18.6, 32 rows 17.8 against 27.2): with 256 keys at most to a split.
+bool many_rows(long rows_per_head, long units, long keys) {
+  if (rows_per_head > 32) return true;
+  if (rows_per_head <= 8 || units > num_sms()) return false;
+  const long splits = num_sms() / units < 16 ? num_sms() / units : 16;
+  return keys <= splits * 256;
+}
 
 bool head_counts_ok(int n_seqs, int max_q, int hq, int hkv, int hd) {
   return n_seqs >= 0 && max_q >= 0 && hkv >= 1 && hkv <= 65536 && hq >= hkv && hq <= 65536 &&
@@ -773,9 +836,11 @@ bool head_counts_ok(int n_seqs, int max_q, int hq, int hkv, int hd) {
 
 extern "C" size_t frt_paged_attention_workspace_size(int n_seqs, int max_q, int hq, int hkv, int hd) {
   if (!frt::head_counts_ok(n_seqs, max_q, hq, hkv, hd)) return 0;
-  if (frt::many_rows(long(max_q) * (hq / hkv)))
-    return frt::attn_many_workspace(hd, n_seqs, max_q, hq, hkv);
-  return frt::with_variant(hd, long(max_q) * (hq / hkv), [](auto v) { return v.workspace(); });
+  const long rows = long(max_q) * (hq / hkv);
+  const size_t many = rows > 8 ? frt::attn_many_workspace(hd, n_seqs, max_q, hq, hkv) : 0;
+  if (rows > 32) return many;
+  const size_t few = frt::with_variant(hd, rows, [](auto v) { return v.workspace(); });
+  return few > many ? few : many;
 }
 
 extern "C" int frt_paged_attention_fp4(const frt_paged_attn_desc* d, void* stream) {
@@ -828,7 +893,7 @@ extern "C" int frt_paged_attention_fp4(const frt_paged_attn_desc* d, void* strea
   a.status = frt::device_status_ptr();
   FRT_REQUIRE(a.status, FRT_ECUDA, "device status word unavailable");
   const long per_head = long(d->max_q) * a.group;
-  if (frt::many_rows(per_head))
+  if (frt::many_rows(per_head, long(d->n_seqs) * d->hkv, long(d->max_pages) * d->page_size))
     return frt::attn_many_launch(a, d->hd, d->workspace, static_cast<cudaStream_t>(stream));
   return frt::with_variant(d->hd, per_head, [&](auto v) {
     using C = typename decltype(v)::C;

@@ -354,13 +354,13 @@ attn_many_kernel(AttnArgs a, int splits, int tiles_max) {
         mx = max32(x[i + 1], max32(x[i], mx));
       }
       const float top = mx == -INFINITY ? mx : mx * c;
-      // the maximum is raised only when a score passes it by more than 2^8
-      // (the weights then stay within fp16), so O is rarely rescaled
-      const bool grow = top > m + 8.0f;
+      // the maximum (kLift below the largest score when it is set) is raised
+      // only when a score passes it by more than kGrow, so O is rarely rescaled
+      const bool grow = top > m + kGrow;
       if (__any_sync(0xffffffffu, grow)) {
-        const float f = grow ? ex2(m - top) : 1.0f;
+        const float f = grow ? ex2(m - (top - kLift)) : 1.0f;
         l2 = mul2(l2, f2_pack(f, f));
-        if (grow) m = top;
+        if (grow) m = top - kLift;
         if (k > 0) {
           // S of tile k vouches for the products up to k - 2, and those of
           // k wait for this warp: the parity names those of k - 1
@@ -715,6 +715,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, int splits, 
 template <int HD>
 struct Many {
   using C = ManyCfg<HD>;
+  static constexpr size_t kHead = 4096;  // the other kernels' counters, which stay zero
   static long tiles(int max_q, int group) { return (long(max_q) * group + C::R - 1) / C::R; }
   static long units(int n_seqs, int max_q, int hq, int hkv) {
     return long(n_seqs) * hkv * tiles(max_q, hq / hkv);
@@ -727,7 +728,7 @@ struct Many {
   }
   static size_t workspace(int n_seqs, int max_q, int hq, int hkv) {
     const int n = splits(n_seqs, max_q, hq, hkv);
-    return n == 1 ? 0 : size_t(units(n_seqs, max_q, hq, hkv)) * n * C::R * (HD + 2) * 4;
+    return n == 1 ? 0 : kHead + size_t(units(n_seqs, max_q, hq, hkv)) * n * C::R * (HD + 2) * 4;
   }
   static int launch(AttnArgs a, void* ws, cudaStream_t st) {
     auto kern = attn_many_kernel<HD>;
@@ -736,7 +737,7 @@ struct Many {
     const long most = (long(a.max_pages) * a.pool.page_size + 127) / 128;
     int n = splits(a.n_seqs, a.max_q, a.hq, a.hkv);
     if (n > most) n = most < 1 ? 1 : int(most);
-    a.partials = static_cast<float*>(ws);
+    a.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kHead);
     const int tm = int(tiles(a.max_q, a.group));
     const long blocks = units(a.n_seqs, a.max_q, a.hq, a.hkv) * n;
     FRT_REQUIRE(blocks <= 0x7fffffffL, FRT_ESHAPE, "n_seqs * max_q * hq is too large");

@@ -172,11 +172,17 @@ def ptr(x):
     return x.data_ptr() or None
 
 
+_raw_stream = _device = None  # torch's, once it is needed
+
+
 def _stream(stream):
     if stream is None:
         # the raw handle: building a Stream object costs as much as a launch
-        import torch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) or None
+        global _raw_stream, _device
+        if _raw_stream is None:
+            import torch
+            _raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
+        return _raw_stream(_device()) or None
     if isinstance(stream, int):
         return stream or None
     return stream.cuda_stream or None

@@ -121,6 +121,11 @@ def attention(q, k, v, L, causal, window, scale):
         a = (w / z) @ np.abs(vv)
         # the weights' fp16 rounding (2^-11), the sums over the keys
         # (2^-23 a step, a step per 16 keys and one per join)
-        e_out[rows, h] = a * (2.0 ** -11 + 2 * d + (L / 16 + 40) * 2.0 ** -23)[:, None] if np.ndim(d) else 0
+        e_out[rows, h] = a * (2.0 ** -11 + 2 * d + (L / 16 + 40) * 2.0 ** -23)[:, None]
+        # weights below 2^-21 of the largest round by up to 2^-32 of it
+        e_out[rows, h] += 2.0 ** -32 * np.abs(vv).sum(0)
+        # the output's own rounding is half a step of the computed value v', not
+        # of v: |bf16(v') - v| <= e + 2^-8 |v'| <= e (1 + 2^-8) + 2^-8 |v|
+        e_out[rows, h] *= 1 + HALF_BF16
         e_lse[rows, h] = d + (L / 16 + 40) * 2.0 ** -23 + np.abs(lse[rows, h]) * 2.0 ** -22
     return out, lse, e_out, e_lse

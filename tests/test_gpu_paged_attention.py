@@ -74,7 +74,7 @@ class Problem:
         max_q = max(1, max(q for q, _ in lens))
         self.nbytes = frt.frt_paged_attention_workspace_size(n, max_q, hq, hkv, hd)
         self.ws = runtime.workspace(self.nbytes)
-        self.counters = max_q * hq // hkv <= 32   # the kernels for few rows keep counters
+        self.counters = self.nbytes > 0   # the head of the workspace holds counters
         self.d = runtime.paged_attn_desc(
             n_seqs=n, rows=self.rows, max_q=max_q, hq=hq, hkv=hkv, hd=hd, page_size=ps, max_pages=self.max_pages,
             n_pages=self.n_pages, causal=int(causal), window=window, sm_scale=self.scale, ld_q=hq * hd + pad,
