@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(256, U == 1 ? 2 : 3) head_kernel(HeadArgs a) {
   pdl_wait();
 
   long pos = live ? row : 0, slot = -1;
-  if (live && a.positions) pos = a.positions[row];
+  if (live && a.rot > 0 && a.positions) pos = a.positions[row];
   if constexpr (TO != kToRows) {
     if (live) slot = a.slots[row];
   }

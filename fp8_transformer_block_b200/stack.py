@@ -13,8 +13,12 @@ then frt_ada_rms_tail on (res, dn, g2).  With on-device modulation, each
 step opens with frt_style_project: the conditioning row through the stacked
 dense projection of all 2L + 1 norms (`_style_stack`), whose bf16 rows the
 layers' producers read at norm slots 2l and 2l + 1 and whose final fp32
-rows the tail reads.  Attention itself is outside this
-library; the stand-in keeps every tensor's shape and the residual moving.
+rows the tail reads.  By default the stand-in keeps every tensor's shape
+and the residual moving in attention's place.  With attention="paged_fp4"
+the layers attend: q/k/v come from the unfused producer and GEMM,
+frt_paged_kv_append rotates q and writes the suffix keys and values behind
+the prefix into 4-bit pages, and frt_paged_attention_fp4 lets every token see
+prefix and suffix; its output takes the stand-in's place.
 Argument marshalling only: every step runs in the CUDA library.
 """
 
@@ -28,7 +32,7 @@ from . import runtime as rt
 
 
 class AdaRmsLayerStack:
-    def __init__(self, w, layers, fin, scales=None, x=None, modulation=None):
+    def __init__(self, w, layers, fin, scales=None, x=None, modulation=None, attention=None):
         """w: a "full" Workload; layers: synth.full_layer_inputs per layer;
         fin: fp32 [3, D] rows of the final norm; scales: per layer dict
         (a_qkv, a_o, a_gu, a_dn), or None to calibrate on the GPU from the
@@ -36,8 +40,12 @@ class AdaRmsLayerStack:
         modulation: None (the layers' own style rows and `fin`), or a dict
         of the stacked projection "w" (bf16 bits [(2L + 1) * 3D, D]), its
         fp32 "bias" and one fp32 conditioning row "cond" [1, D]: every step
-        then computes all norms' rows on the device (`fin` is unused)."""
-        assert w.hq * w.hd == w.D, "the attention stand-in needs hq * hd == D"
+        then computes all norms' rows on the device (`fin` is unused).
+        attention: None (the stand-in), or "paged_fp4" (each layer's keys and
+        values, prefix included, in 4-bit pages of 16 tokens; their static
+        scales are calibrated with the others, or given as a_k and a_v)."""
+        assert w.hq * w.hd == w.D, "the attention output needs hq * hd == D"
+        assert attention in (None, "paged_fp4"), attention
         self.w = w
         B, M, D, H = w.B, w.M, w.D, w.H
         rows = B * M
@@ -103,9 +111,15 @@ class AdaRmsLayerStack:
                             frt.frt_gemm_workspace_size(rows, 2 * H, D),
                             frt.frt_gemm_workspace_size(rows, D, H))
         self.ws = rt.workspace(self.ws_bytes)
+        self.att = None
+        if attention:
+            self._paged(N)
         if scales is None:
             scales = self.calibrate(x)
         self.scales = scales
+        if self.att:
+            for l, sc in enumerate(scales):
+                self._load_prefix(l, sc["a_k"], sc["a_v"])
         self.sdev = [{k: rt.scale_dev(v) for k, v in sc.items()} for sc in scales]
         self._build()
 
@@ -135,12 +149,87 @@ class AdaRmsLayerStack:
                 w_scale_dn=ly["dn"].w_scale, bias_dn=None, out=self.dn[l % 2],
                 workspace=self.ws, workspace_bytes=self.ws_bytes))
 
+    PAGE = 16  # tokens; the prefix need not end with a page
+
+    def _paged(self, N):
+        """The layers' page pools (sequence b of a layer: consecutive pages)
+        and the descriptors' shared parts."""
+        w = self.w
+        per = (w.P + w.M + self.PAGE - 1) // self.PAGE
+        dev = "cuda"
+        pages = torch.arange(w.B * per, device=dev, dtype=torch.int32).view(w.B, per)
+        at = torch.arange(w.P + w.M, device=dev)
+        slots = (pages.long()[:, at // self.PAGE] * self.PAGE + at % self.PAGE)
+        rope = torch.empty(w.M, w.hd, device=dev)
+        frt.frt_build_rope_table_scaled(w.M, w.hd, w.P, w.theta, frt.FRT_ROPE_SCALE_NONE, 1.0, 0.0,
+                                        0.0, 0.0, 1.0, rope)
+        nbytes = frt.frt_paged_attention_workspace_size(w.B, w.M, w.hq, w.hkv, w.hd)
+        self.att = {
+            "per": per, "pages": pages, "rope": rope,
+            "prefix": slots[:, :w.P].contiguous(), "suffix": slots[:, w.P:].contiguous(),
+            "pos": torch.arange(w.M, device=dev, dtype=torch.int32).repeat(w.B),
+            "len": torch.full((w.B,), w.P + w.M, device=dev, dtype=torch.int32),
+            "qkv": rt.empty_bf16(self.rows, N), "out": rt.empty_bf16(self.rows, w.D),
+            "pool": [rt.kv_pool(w.B * per, w.hkv, self.PAGE, w.hd) for _ in self.lay],
+            "scale": [torch.ones(2, device=dev) for _ in self.lay],
+            "ws": rt.workspace(nbytes), "ws_bytes": nbytes}
+        self.att["append"] = [self._append_desc(l, self.att["qkv"], self.rows, w.hq, w.hd,
+                                                self.att["suffix"], self.q) for l in range(self.L)]
+        self.att["attend"] = [rt.paged_attn_desc(
+            n_seqs=w.B, rows=self.rows, max_q=w.M, hq=w.hq, hkv=w.hkv, hd=w.hd, page_size=self.PAGE,
+            max_pages=per, n_pages=w.B * per, causal=0, window=0, sm_scale=w.hd ** -0.5, q=self.q,
+            ld_q=w.D, pool=self.att["pool"][l], page_table=pages, cu_rows=None,
+            kv_len=self.att["len"], k_scale=self.att["scale"][l][0:1],
+            v_scale=self.att["scale"][l][1:2], out=self.att["out"], ld_out=w.D, lse=None,
+            workspace=self.att["ws"], workspace_bytes=nbytes) for l in range(self.L)]
+
+    def _append_desc(self, l, qkv, rows, hq, rot, slots, q_out):
+        w, a = self.w, self.att
+        return rt.qk_rope_desc(
+            rows=rows, hq=hq, hkv=w.hkv, hd=w.hd, rot=rot, layout=frt.FRT_ROPE_PAIRS, eps=w.eps,
+            qkv=qkv, ld_qkv=qkv.shape[1], rope=a["rope"] if rot else None, n_pos=w.M,
+            positions=a["pos"] if rot else None,
+            q_out=q_out, ld_q=w.D, format=frt.FRT_PAGE_E2M1, page_size=self.PAGE,
+            n_pages=w.B * a["per"], pool=a["pool"][l], slots=slots,
+            k_scale=a["scale"][l][0:1], v_scale=a["scale"][l][1:2])
+
+    def _prefix_rows(self, l):
+        """The host's prefix keys (pairs made adjacent) and values as rows
+        [B * P, 2 * hkv * hd], rotated already."""
+        w, ly = self.w, self.lay[l]
+        frt.frt_prefix_copy_kv(w.B, w.hkv, w.hd, w.P, w.T, w.P, ly["pk"], ly["pv"], 1, ly["kc"],
+                               ly["vc"])
+        return torch.cat([c[:, :w.P].reshape(w.B * w.P, -1) for c in (ly["kc"], ly["vc"])], 1)
+
+    def _load_prefix(self, l, a_k, a_v):
+        self.att["scale"][l].copy_(torch.tensor([a_k, a_v]))
+        if self.w.P:
+            x = self._prefix_rows(l)
+            frt.frt_paged_kv_append(self._append_desc(l, x, x.shape[0], 0, 0, self.att["prefix"],
+                                                      None))
+            torch.cuda.synchronize()  # x goes
+
+    def _attend(self, l, style, delta, gate, gate_stride, scale):
+        """One layer's attention half: producer, GEMM, append, attention."""
+        w, a, ly = self.w, self.att, self.lay[l]
+        frt.frt_ada_norm_quant_fp8(frt.FRT_NORM_ADARMS, self.rows, w.D, w.eps, self.res, delta, gate,
+                                   gate_stride, None, style, 0, None, None, 0, None, 0, 0, scale,
+                                   self.x8, self.g1)
+        N = a["qkv"].shape[1]
+        frt.frt_packed_fp8_gemm(self.rows, N, w.D, self.x8, ly["qkv"].w8, scale, ly["qkv"].w_scale,
+                                None, frt.FRT_EPI_BF16, a["qkv"], N, None, self.ws, self.ws_bytes)
+        frt.frt_paged_kv_append(a["append"][l])
+        frt.frt_paged_attention_fp4(a["attend"][l])
+
     def _out_project(self, l, scale):
         D, rows = self.w.D, self.rows
-        frt.frt_quantize_fp8_static(rows, D, self.q, D, scale, self.o8)
+        frt.frt_quantize_fp8_static(rows, D, self._att2(), D, scale, self.o8)
         ly = self.lay[l]
         frt.frt_packed_fp8_gemm(rows, D, D, self.o8, ly["o"].w8, scale, ly["o"].w_scale, None,
                                 frt.FRT_EPI_BF16, self.dn_o, D, None, self.ws, self.ws_bytes)
+
+    def _att2(self):
+        return self.att["out"] if self.att else self.q
 
     def _project(self):
         m, D = self.mod, self.w.D
@@ -157,7 +246,13 @@ class AdaRmsLayerStack:
         if self.mod is not None:
             self._project()
         for l in range(self.L):
-            frt.frt_chain_layer(self.cdesc[l])
+            if self.att:
+                first, before = l == 0, (l - 1) % 2
+                self._attend(l, self.lay[l]["st_attn"], self.zero if first else self.dn[before],
+                             self.zero if first else self.g2[before], 0 if first else self.w.D,
+                             self.sdev[l]["a_qkv"])
+            else:
+                frt.frt_chain_layer(self.cdesc[l])
             self._out_project(l, self.sdev[l]["a_o"])
             frt.frt_ffn_layer(self.fdesc[l])
         last = (self.L - 1) % 2
@@ -205,7 +300,22 @@ class AdaRmsLayerStack:
                 w.B, w.M, D, w.hq, w.hkv, w.hd, w.P, w.T, self.x8, ly["qkv"].w8,
                 rt.scale_dev(sc["a_qkv"]), ly["qkv"].w_scale, None, self.rope, self.q,
                 ly["kc"], ly["vc"], self.ws, self.ws_bytes)
-            sc["a_o"] = amax_of(lambda a: frt.frt_quantize_fp8_static(rows, D, self.q, D, one,
+            if self.att:
+                # the page scales: the bf16 keys and values of this batch and
+                # the prefix, whose largest is to meet the largest block scale
+                if w.P:
+                    self._prefix_rows(l)
+                kv = torch.cat([c[:, :w.P + w.M].reshape(w.B * (w.P + w.M), 1, -1)
+                                for c in (ly["kc"], ly["vc"])], 1).float().abs().amax((0, 2))
+                sc["a_k"], sc["a_v"] = (max(float(v) / 2688.0, 1e-8) for v in kv)
+                self._load_prefix(l, sc["a_k"], sc["a_v"])
+                frt.frt_packed_fp8_gemm(rows, self.att["qkv"].shape[1], D, self.x8, ly["qkv"].w8,
+                                        rt.scale_dev(sc["a_qkv"]), ly["qkv"].w_scale, None,
+                                        frt.FRT_EPI_BF16, self.att["qkv"],
+                                        self.att["qkv"].shape[1], None, self.ws, self.ws_bytes)
+                frt.frt_paged_kv_append(self.att["append"][l])
+                frt.frt_paged_attention_fp4(self.att["attend"][l])
+            sc["a_o"] = amax_of(lambda a: frt.frt_quantize_fp8_static(rows, D, self._att2(), D, one,
                                                                       junk, a))
             self._out_project(l, rt.scale_dev(sc["a_o"]))
             snap = self.res.clone()

@@ -539,7 +539,7 @@ typedef struct frt_qk_rope_desc {
   const float* rope;      /* [n_pos, rot] fp32 (frt_build_rope_table_scaled) */
   int n_pos;
   const int* positions;   /* device [rows]: table row of each token;
-                             NULL = 0, 1, 2, ...                            */
+                             NULL = 0, 1, 2, ...; not read when rot is 0    */
   frt_bf16* q_out; long ld_q;         /* [rows, hq * hd], strided           */
   frt_bf16* k_out; long ld_k;         /* [rows, hkv * hd], strided          */
   frt_bf16* v_out; long ld_v;         /* [rows, hkv * hd] (frt_paged_kv_read) */
