@@ -31,9 +31,9 @@ struct ManyCfg {
   // four warpgroups: QT of softmax, the rest but one of widening, and the MMAs
   static constexpr int kThreads = 512;
   // registers a thread of each (setmaxnreg), of the launch's 512 x 128
-  static constexpr int kRegsSoftmax = QT == 2 ? 184 : 184;
+  static constexpr int kRegsSoftmax = 184;
   static constexpr int kRegsWide = QT == 2 ? 80 : 128;
-  static constexpr int kRegsMma = QT == 2 ? 64 : 64;
+  static constexpr int kRegsMma = 64;
   static_assert(128 * (QT * kRegsSoftmax + (3 - QT) * kRegsWide + kRegsMma) <= 512 * 128,
                 "the shares exceed the launch's registers");
   static constexpr int kQBytes = 128 * HD * 2;     // one row tile
@@ -205,10 +205,6 @@ attn_many_kernel(AttnArgs a, int splits, int tiles_max) {
     fence_barrier_init();
   }
   pdl_wait();
-  if (warp == 12) {
-    tmem_alloc(tmem_ptr, C::kTmem);
-    tmem_relinquish();
-  }
   long b = blockIdx.x;
   const long part_index = b;
   const int split = int(b % splits);
@@ -219,7 +215,11 @@ attn_many_kernel(AttnArgs a, int splits, int tiles_max) {
   // causal tiles with the most keys first
   const int tile = tiles_max - 1 - int(b / a.n_seqs);
   const Seq q = load_seq<R, KVT>(a, s, tile == 0 && head == 0 && split == 0 && tid == 0);
-  const bool any_rows = tile < q.tiles;
+  if (tile >= q.tiles) return;   // the sequence is shorter than the longest
+  if (warp == 12) {
+    tmem_alloc(tmem_ptr, C::kTmem);
+    tmem_relinquish();
+  }
 
   int begin[QT], end[QT], lo = 0x7fffffff, hi = 0;
 #pragma unroll
@@ -242,10 +242,6 @@ attn_many_kernel(AttnArgs a, int splits, int tiles_max) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_ptr;
-  if (!any_rows) {
-    if (warp == 12) tmem_dealloc(tmem, C::kTmem);
-    return;
-  }
 
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (mbar_wait_bounded(bar, parity, kAttnWaitNs, abort_flag)) return true;

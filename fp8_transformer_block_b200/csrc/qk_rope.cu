@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(256, U == 1 ? 2 : 3) head_kernel(HeadArgs a) {
   const uint32_t n_q = uint32_t(a.rows) * a.q_units, n_k = uint32_t(a.rows) * kv_units;
   const bool is_q = unit < n_q, is_v = unit >= n_q + n_k;
   unit -= is_q ? 0 : is_v ? n_q + n_k : n_q;
-  const uint32_t per_row = is_q ? a.q_units : kv_units;
+  const uint32_t per_row = max(1u, is_q ? uint32_t(a.q_units) : kv_units);
   const uint32_t row32 = unit / per_row;
   const long row = row32;
   const int j0 = int(unit - row32 * per_row) * U;  // of the kind's heads
@@ -272,13 +272,18 @@ __global__ void __launch_bounds__(256, U == 1 ? 2 : 3) head_kernel(HeadArgs a) {
       }
     }
     if (rotates) {
+      // scalar operations with their own roundings: paired products and sums
+      // came out fused, and a key next to a 4-bit border must not depend on that
       if (half) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint64_t c = f2_pack(cs[4 * j], cs[4 * j + 2]), s = f2_pack(cs[4 * j + 1], cs[4 * j + 3]);
-          const uint64_t u0 = y[0][j], u1 = y[1][j];
-          y[0][j] = sub2(mul2(u0, c), mul2(u1, s));
-          y[1][j] = add2(mul2(u0, s), mul2(u1, c));
+        for (int j = 0; j < 8; ++j) {
+          const float c = cs[2 * j], s = cs[2 * j + 1];
+          uint64_t &v0 = y[0][j / 2], &v1 = y[1][j / 2];
+          const float e0 = j % 2 ? f2_hi(v0) : f2_lo(v0), e1 = j % 2 ? f2_hi(v1) : f2_lo(v1);
+          const float r0 = __fsub_rn(__fmul_rn(e0, c), __fmul_rn(e1, s));
+          const float r1 = __fadd_rn(__fmul_rn(e0, s), __fmul_rn(e1, c));
+          v0 = j % 2 ? f2_pack(f2_lo(v0), r0) : f2_pack(r0, f2_hi(v0));
+          v1 = j % 2 ? f2_pack(f2_lo(v1), r1) : f2_pack(r1, f2_hi(v1));
         }
       } else {
 #pragma unroll

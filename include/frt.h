@@ -631,6 +631,9 @@ size_t frt_paged_attention_workspace_size(int n_seqs, int max_q, int hq, int hkv
  * codes times their block scales are exact in fp16, q is scaled by a power
  * of two into it, the weights are rounded to fp16 once; softmax statistics
  * and sums in fp32; results are the same from call to call.
+ * Sequences of very different query counts are better called apart: every
+ * sequence is scheduled like one of max_q rows, of which a short one's share
+ * ends at once.
  * workspace (NULL where the size is 0): zero-filled once before its first use; every completed call
  * leaves its counters at zero.  Calls (and captured graphs) that share one
  * must not overlap.  Only the pages that hold a sequence's first kv_len

@@ -129,6 +129,34 @@ def test_norm_rope_in_place_equals_out_of_place(rt):
     assert torch.equal(v, keep2[0][:, 8 * 128:])
 
 
+def test_norm_of_special_rows(rt):
+    """Infinite, NaN, huge and all-zero heads: as the formula has them, and
+    only in their own head."""
+    frt, runtime, torch = rt
+    hd, heads = 64, 6
+    x = np.random.default_rng(9).standard_normal((3, heads * hd), dtype=np.float32)
+    bits = bf16_bits(x).reshape(3, heads, hd)
+    bits[0, 0, 5] = 0x7F80            # inf: the others 0, itself NaN
+    bits[0, 1, 7] = 0x7FC0            # NaN
+    bits[1, 2] = 0                    # zeros: 0 / sqrt(eps)
+    bits[2, 3] = 0x7F00               # 2^127 each: the mean square is past fp32
+    w = runtime.bf16_dev(np.full(hd, 0x3F80, np.uint16))
+    dev = runtime.bf16_dev(bits.reshape(3, -1))
+    out = torch.zeros(3, heads * hd, dtype=torch.bfloat16, device="cuda")
+    d = runtime.qk_rope_desc(rows=3, hq=heads, hkv=0, hd=hd, rot=0, layout=1, eps=1e-6, qkv=dev,
+                             ld_qkv=heads * hd, q_norm=w, q_out=out, ld_q=heads * hd)
+    frt.frt_qk_norm_rope(d)
+    torch.cuda.synchronize()
+    g = bf16_value(runtime.bf16_host(out)).reshape(3, heads, hd)
+    assert np.isnan(g[0, 0, 5]) and np.all(np.delete(g[0, 0], 5) == 0)
+    assert np.all(np.isnan(g[0, 1]))
+    assert np.all(g[1, 2] == 0) and np.all(g[2, 3] == 0)
+    ok = np.ones((3, heads), bool)
+    ok[0, 0] = ok[0, 1] = ok[1, 2] = ok[2, 3] = False
+    v, size = ref.norm_rotate(bf16_value(bits), np.ones(hd), 1e-6, None, None, 0, True)
+    assert np.all((np.abs(g - v) <= ref.HALF_BF16 * np.abs(v) + 10 * ref.F32 * size)[ok])
+
+
 def test_positions_outside_the_table(rt):
     frt, runtime, torch = rt
     d, keep, q, k, want, _ = run_heads(rt, np.random.default_rng(2), 9, 2, 1, 64, 64, True, False, 0, n_pos=32)
