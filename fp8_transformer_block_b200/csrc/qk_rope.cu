@@ -158,215 +158,241 @@ __device__ __forceinline__ uint32_t quantise8(const uint64_t (&y)[4], uint8_t s8
 // idle); a group of LANES lanes takes U consecutive heads of one kind (q, k
 // or v) of one row, one after another, the next one's elements under way.
 // Bound by bytes: 8192 rows of 24 + 24 heads of 128, normed and rotated, run
-// at 4.6 TB/s (44 us); 24 warps an SM (80 registers) measured better than 16
+// at 4.5 TB/s (45 us); 24 warps an SM (80 registers) measured better than 16
 // with more registers (54 us) and than 32 with spills (63 us), one loop over
-// the heads better than U heads in registers at once (58 us).
+// the heads better than U heads in registers at once (58 us).  Into pages, a
+// unit's work hangs on its slot as well, and the blocks go from unit to unit
+// with the next one's index words and first head under way (16381 rows of 32 +
+// 8 + 8 heads of 128 into 4-bit pages: 109 us against 129; the rows form loses
+// by it, 51 us against 45).
 template <int LANES, int U, int TO>
-__global__ void __launch_bounds__(256, U == 1 ? 2 : 3) head_kernel(HeadArgs a) {
+__global__ void __launch_bounds__(256, U == 1 || TO != kToRows ? 2 : 3) head_kernel(HeadArgs a) {
   const int lane = int(threadIdx.x) % LANES;
   // the group's lanes of the warp: other groups may be at other kinds of heads
   const uint32_t group = (0xffffffffu >> (32 - LANES)) << (threadIdx.x % 32 / LANES * LANES);
-  // all rows' q heads, then all k heads, then all v heads: a warp's groups
-  // are at one kind, and so on one path
-  uint32_t unit = uint32_t(blockIdx.x) * (256 / LANES) + threadIdx.x / LANES;
-  const uint32_t kv_units = (uint32_t(a.hkv) + U - 1) / U;
-  const uint32_t n_q = uint32_t(a.rows) * a.q_units, n_k = uint32_t(a.rows) * kv_units;
-  const bool is_q = unit < n_q, is_v = unit >= n_q + n_k;
-  unit -= is_q ? 0 : is_v ? n_q + n_k : n_q;
-  const uint32_t per_row = max(1u, is_q ? uint32_t(a.q_units) : kv_units);
-  const uint32_t row32 = unit / per_row;
-  const long row = row32;
-  const int j0 = int(unit - row32 * per_row) * U;  // of the kind's heads
-  const int jn = min(U, (is_q ? a.hq : a.hkv) - j0);
-  const int h0 = j0 + (is_q ? 0 : a.hq) + (is_v ? a.hkv : 0);
-  const bool live = row < a.rows && (TO != kToRows || !is_v);  // the whole group's
   Pieces at;
   at.turn = a.rot / 16;
   at.rest = (a.hd / 8 - 2 * at.turn + 1) / 2;
   const int p0 = at.piece(lane, 0), p1 = at.piece(lane, 1);
-  const bool has0 = live && p0 * 8 < a.hd && lane < at.turn + at.rest;
+  const bool has0 = p0 * 8 < a.hd && lane < at.turn + at.rest;
   const bool has1 = has0 && p1 * 8 < a.hd;
+  const bool half = a.layout == FRT_ROPE_HALF;
+  // all rows' q heads, then all k heads, then all v heads: a warp's groups
+  // are at one kind, and so on one path
+  const uint32_t kv_units = (uint32_t(a.hkv) + U - 1) / U;
+  const uint32_t n_q = uint32_t(a.rows) * a.q_units, n_k = uint32_t(a.rows) * kv_units;
+  const uint32_t n_units = n_q + n_k * (TO == kToRows ? 1 : 2);
+  const uint32_t stride = gridDim.x * (256 / LANES);
+  uint32_t unit = uint32_t(blockIdx.x) * (256 / LANES) + threadIdx.x / LANES;
   pdl_trigger();
   pdl_wait();
+  if (unit >= n_units) return;   // the whole group
 
-  long pos = live ? row : 0, slot = -1;
-  if (live && a.rot > 0 && a.positions) pos = a.positions[row];
-  if constexpr (TO != kToRows) {
-    if (live) slot = a.slots[row];
-  }
-  const uint16_t* src = a.qkv + row * a.ld_qkv + long(h0) * a.hd;
+  // what is loaded ahead for a unit: its row's index words, its first head
+  struct Ahead {
+    uint32_t row;
+    int kind, j0;      // 0 q, 1 k, 2 v; the first of the kind's heads
+    int pos;
+    long slot;
+    const uint16_t* src;
+  } next;
   uint4 n0 = make_uint4(0, 0, 0, 0), n1 = n0;   // the next head's pieces
-  if (has0) n0 = *reinterpret_cast<const uint4*>(src + p0 * 8);
-  if (has1) n1 = *reinterpret_cast<const uint4*>(src + p1 * 8);
-
-  const uint16_t* w = is_v ? nullptr : is_q ? a.q_norm : a.k_norm;
-  uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
-  if (w) {
-    if (has0) w0 = *reinterpret_cast<const uint4*>(w + p0 * 8);
-    if (has1) w1 = *reinterpret_cast<const uint4*>(w + p1 * 8);
-  }
-  float static_scale = 1.0f;
-  if constexpr (TO == kToFp4Pages) static_scale = *(is_v ? a.v_scale : a.k_scale);
-
-  const bool bad_pos = a.rot > 0 && (pos < 0 || pos >= a.n_pos);
-  bool bad_slot = false;
-  if constexpr (TO != kToRows) bad_slot = slot >= a.pool.slots();
-  if (live && (bad_pos || bad_slot) && lane == 0) atomicExch(a.status, FRT_ERANGE);
-
-  // this lane's cos and sin: of the 8 pairs (piece 0, piece 1), or of the 4
-  // adjacent pairs of each piece
-  const bool half = a.layout == FRT_ROPE_HALF;
-  const bool rotates = live && lane < at.turn && !bad_pos && !is_v;
-  float cs[16];
-  if (rotates) {
-    const float* t = a.rope + pos * a.rot;
-    const int o0 = half ? lane * 16 : p0 * 8, o1 = half ? lane * 16 + 8 : p1 * 8;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float4 v = *reinterpret_cast<const float4*>(t + (j < 2 ? o0 : o1) + j % 2 * 4);
-      cs[4 * j] = v.x; cs[4 * j + 1] = v.y; cs[4 * j + 2] = v.z; cs[4 * j + 3] = v.w;
-    }
-  }
-
-  // the next head's pieces, and on to the one after it
-  auto advance = [&](int u, uint4& o0, uint4& o1) {
-    o0 = n0;
-    o1 = n1;
-    if (u + 1 < jn) {
-      src += a.hd;
-      if (has0) n0 = *reinterpret_cast<const uint4*>(src + p0 * 8);
-      if (has1) n1 = *reinterpret_cast<const uint4*>(src + p1 * 8);
-    }
+  auto look_ahead = [&](uint32_t x) {
+    next.kind = x < n_q ? 0 : x < n_q + n_k ? 1 : 2;
+    x -= next.kind == 0 ? 0 : next.kind == 1 ? n_q : n_q + n_k;
+    const uint32_t per_row = next.kind == 0 ? uint32_t(a.q_units) : kv_units;
+    next.row = x / per_row;
+    next.j0 = int(x - next.row * per_row) * U;
+    next.pos = a.rot > 0 ? a.positions ? a.positions[next.row] : int(next.row) : 0;
+    if constexpr (TO != kToRows) next.slot = a.slots[next.row];
+    next.src = a.qkv + long(next.row) * a.ld_qkv +
+               long(next.j0 + (next.kind > 0 ? a.hq : 0) + (next.kind > 1 ? a.hkv : 0)) * a.hd;
+    if (has0) n0 = *reinterpret_cast<const uint4*>(next.src + p0 * 8);
+    if (has1) n1 = *reinterpret_cast<const uint4*>(next.src + p1 * 8);
   };
-  // the norm and the rotation of one head, rounded to bf16
-  auto norm_rotate = [&](uint4& o0, uint4& o1) {
-    if (!w && a.rot == 0) return;
-    uint64_t y[2][4];
-    unpack8_f2(o0, y[0]);
-    unpack8_f2(o1, y[1]);
+  look_ahead(unit);
+
+#pragma unroll 1
+  for (;;) {
+    const Ahead now = next;
+    const long row = now.row, slot = TO != kToRows ? now.slot : 0;
+    const int j0 = now.j0, pos = now.pos;
+    const bool is_q = now.kind == 0, is_v = now.kind == 2;
+    const int jn = min(U, (is_q ? a.hq : a.hkv) - j0);
+    const uint16_t* src = now.src;
+    const uint16_t* w = is_v ? nullptr : is_q ? a.q_norm : a.k_norm;
+    uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
     if (w) {
-      // the sum of squares in fp64: a key next to a 4-bit border must not
-      // depend on the order of its summands
-      double s = 0.0, s1 = 0.0;
+      if (has0) w0 = *reinterpret_cast<const uint4*>(w + p0 * 8);
+      if (has1) w1 = *reinterpret_cast<const uint4*>(w + p1 * 8);
+    }
+    float static_scale = 1.0f;
+    if constexpr (TO == kToFp4Pages) static_scale = *(is_v ? a.v_scale : a.k_scale);
+
+    const bool bad_pos = a.rot > 0 && (pos < 0 || pos >= a.n_pos);
+    bool bad_slot = false;
+    if constexpr (TO != kToRows) bad_slot = slot >= a.pool.slots();
+    // this lane's cos and sin: of the 8 pairs (piece 0, piece 1), or of the 4
+    // adjacent pairs of each piece
+    const bool rotates = lane < at.turn && !bad_pos && !is_v;
+    float cs[16];
+    if (rotates) {
+      const float* t = a.rope + long(pos) * a.rot;
+      const int o0 = half ? lane * 16 : p0 * 8, o1 = half ? lane * 16 + 8 : p1 * 8;
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int j = 0; j < 4; ++j) {
+        const float4 v = *reinterpret_cast<const float4*>(t + (j < 2 ? o0 : o1) + j % 2 * 4);
+        cs[4 * j] = v.x; cs[4 * j + 1] = v.y; cs[4 * j + 2] = v.z; cs[4 * j + 3] = v.w;
+      }
+    }
+    if ((bad_pos || bad_slot) && lane == 0) atomicExch(a.status, FRT_ERANGE);
+
+    // a head's pieces; the next one's, or the next unit's first, under way
+    const bool more = TO != kToRows && n_units - unit > stride;
+    auto advance = [&](int u, uint4& o0, uint4& o1) {
+      o0 = n0;
+      o1 = n1;
+      if (u + 1 < jn) {
+        src += a.hd;
+        if (has0) n0 = *reinterpret_cast<const uint4*>(src + p0 * 8);
+        if (has1) n1 = *reinterpret_cast<const uint4*>(src + p1 * 8);
+      } else if (more) {
+        look_ahead(unit + stride);
+      }
+    };
+    // the norm and the rotation of one head, rounded to bf16
+    auto norm_rotate = [&](uint4& o0, uint4& o1) {
+      if (!w && a.rot == 0) return;
+      uint64_t y[2][4];
+      unpack8_f2(o0, y[0]);
+      unpack8_f2(o1, y[1]);
+      if (w) {
+        // the sum of squares in fp64: a key next to a 4-bit border must not
+        // depend on the order of its summands
+        double s = 0.0, s1 = 0.0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const double lo = f2_lo(y[i][j]), hi = f2_hi(y[i][j]);
+            s = fma(lo, lo, s);
+            s1 = fma(hi, hi, s1);
+          }
+        s += s1;
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o >>= 1) s += __shfl_xor_sync(group, s, o, LANES);
+        const float m = __fadd_rn(float(s * a.inv_hd), a.eps);
+        const float r = __frcp_rn(__fsqrt_rn(m));
+        uint64_t wv[2][4];
+        unpack8_f2(w0, wv[0]);
+        unpack8_f2(w1, wv[1]);
+        const uint64_t r2 = f2_pack(r, r);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const double lo = f2_lo(y[i][j]), hi = f2_hi(y[i][j]);
-          s = fma(lo, lo, s);
-          s1 = fma(hi, hi, s1);
-        }
-      s += s1;
-#pragma unroll
-      for (int o = LANES / 2; o > 0; o >>= 1) s += __shfl_xor_sync(group, s, o, LANES);
-      const float m = __fadd_rn(float(s * a.inv_hd), a.eps);
-      const float r = __frcp_rn(__fsqrt_rn(m));
-      uint64_t wv[2][4];
-      unpack8_f2(w0, wv[0]);
-      unpack8_f2(w1, wv[1]);
-      const uint64_t r2 = f2_pack(r, r);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        y[0][j] = mul2(mul2(y[0][j], r2), wv[0][j]);
-        y[1][j] = mul2(mul2(y[1][j], r2), wv[1][j]);
-      }
-    }
-    if (rotates) {
-      // scalar operations with their own roundings: paired products and sums
-      // came out fused, and a key next to a 4-bit border must not depend on that
-      if (half) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float c = cs[2 * j], s = cs[2 * j + 1];
-          uint64_t &v0 = y[0][j / 2], &v1 = y[1][j / 2];
-          const float e0 = j % 2 ? f2_hi(v0) : f2_lo(v0), e1 = j % 2 ? f2_hi(v1) : f2_lo(v1);
-          const float r0 = __fsub_rn(__fmul_rn(e0, c), __fmul_rn(e1, s));
-          const float r1 = __fadd_rn(__fmul_rn(e0, s), __fmul_rn(e1, c));
-          v0 = j % 2 ? f2_pack(f2_lo(v0), r0) : f2_pack(r0, f2_hi(v0));
-          v1 = j % 2 ? f2_pack(f2_lo(v1), r1) : f2_pack(r1, f2_hi(v1));
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          uint64_t& v = y[j / 4][j % 4];
-          const float e0 = f2_lo(v), e1 = f2_hi(v), c = cs[2 * j], s = cs[2 * j + 1];
-          v = f2_pack(__fsub_rn(__fmul_rn(e0, c), __fmul_rn(e1, s)),
-                      __fadd_rn(__fmul_rn(e0, s), __fmul_rn(e1, c)));
+          y[0][j] = mul2(mul2(y[0][j], r2), wv[0][j]);
+          y[1][j] = mul2(mul2(y[1][j], r2), wv[1][j]);
         }
       }
-    }
-    o0 = pack8_bf16_f2(y[0]);
-    o1 = pack8_bf16_f2(y[1]);
-  };
+      if (rotates) {
+        // scalar operations with their own roundings: paired products and sums
+        // came out fused, and a key next to a 4-bit border must not depend on that
+        if (half) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float c = cs[2 * j], s = cs[2 * j + 1];
+            uint64_t &v0 = y[0][j / 2], &v1 = y[1][j / 2];
+            const float e0 = j % 2 ? f2_hi(v0) : f2_lo(v0), e1 = j % 2 ? f2_hi(v1) : f2_lo(v1);
+            const float r0 = __fsub_rn(__fmul_rn(e0, c), __fmul_rn(e1, s));
+            const float r1 = __fadd_rn(__fmul_rn(e0, s), __fmul_rn(e1, c));
+            v0 = j % 2 ? f2_pack(f2_lo(v0), r0) : f2_pack(r0, f2_hi(v0));
+            v1 = j % 2 ? f2_pack(f2_lo(v1), r1) : f2_pack(r1, f2_hi(v1));
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            uint64_t& v = y[j / 4][j % 4];
+            const float e0 = f2_lo(v), e1 = f2_hi(v), c = cs[2 * j], s = cs[2 * j + 1];
+            v = f2_pack(__fsub_rn(__fmul_rn(e0, c), __fmul_rn(e1, s)),
+                        __fadd_rn(__fmul_rn(e0, s), __fmul_rn(e1, c)));
+          }
+        }
+      }
+      o0 = pack8_bf16_f2(y[0]);
+      o1 = pack8_bf16_f2(y[1]);
+    };
 
-  if (TO == kToRows || is_q) {
-    uint16_t* dst = (is_q ? a.q_out + row * a.ld_q : a.k_out + row * a.ld_k) + long(j0) * a.hd;
+    if (TO == kToRows || is_q) {
+      uint16_t* dst = (is_q ? a.q_out + row * a.ld_q : a.k_out + row * a.ld_k) + long(j0) * a.hd;
 #pragma unroll 1
-    for (int u = 0; u < jn; ++u, dst += a.hd) {
-      uint4 o0, o1;
-      advance(u, o0, o1);
-      norm_rotate(o0, o1);
-      if (has0 && !bad_pos) *reinterpret_cast<uint4*>(dst + p0 * 8) = o0;
-      if (has1 && !bad_pos) *reinterpret_cast<uint4*>(dst + p1 * 8) = o1;
-    }
-    return;
-  }
-  if (slot < 0 || bad_slot || bad_pos) return;   // the group's
-  uint8_t* rec = a.pool.record(slot, j0);
-  const long row_in = a.pool.row(slot);
-  if constexpr (TO == kToBf16Pages) {
-    rec += ((is_v ? a.pool.page_size : 0) + row_in) * a.hd * 2;
-#pragma unroll 1
-    for (int u = 0; u < jn; ++u, rec += a.pool.record_bytes) {
-      uint4 o0, o1;
-      advance(u, o0, o1);
-      if (!is_v) norm_rotate(o0, o1);
-      if (has0) *reinterpret_cast<uint4*>(rec + p0 * 16) = o0;
-      if (has1) *reinterpret_cast<uint4*>(rec + p1 * 16) = o1;
-    }
-  }
-  if constexpr (TO == kToFp4Pages) {
-    const float rk = __frcp_rn(static_scale);
-    const uint64_t rk2 = f2_pack(rk, rk);
-    rec += is_v ? a.pool.record_bytes / 2 : 0;
-    const long scales = long(a.pool.page_size) * (a.hd / 2) + row_in * (a.hd / 16);
-    // a block of 16 is two neighbouring pieces: who holds the other
-    int lane0, lane1, slot0, slot1;
-    at.find(p0 ^ 1, &lane0, &slot0);
-    at.find(p1 ^ 1, &lane1, &slot1);
-#pragma unroll 1
-    for (int u = 0; u < jn; ++u, rec += a.pool.record_bytes) {
-      uint4 o0, o1;
-      advance(u, o0, o1);
-      if (!is_v) norm_rotate(o0, o1);
-      uint64_t y[2][4];
-      unpack8_f2(o0, y[0]);  // what is cached is the bf16 key
-      unpack8_f2(o1, y[1]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        y[0][j] = mul2(y[0][j], rk2);
-        y[1][j] = mul2(y[1][j], rk2);
+      for (int u = 0; u < jn; ++u, dst += a.hd) {
+        uint4 o0, o1;
+        advance(u, o0, o1);
+        norm_rotate(o0, o1);
+        if (has0 && !bad_pos) *reinterpret_cast<uint4*>(dst + p0 * 8) = o0;
+        if (has1 && !bad_pos) *reinterpret_cast<uint4*>(dst + p1 * 8) = o1;
       }
-      float big0 = absmax8(y[0]), big1 = absmax8(y[1]);
-      const float a0 = __shfl_sync(group, big0, lane0, LANES), a1 = __shfl_sync(group, big1, lane0, LANES);
-      const float b0 = __shfl_sync(group, big0, lane1, LANES), b1 = __shfl_sync(group, big1, lane1, LANES);
-      big0 = fmaxf(big0, slot0 ? a1 : a0);
-      big1 = fmaxf(big1, slot1 ? b1 : b0);
-      if (__any_sync(group, fmaxf(big0, big1) > 8192.0f)) {
-        // far past saturation: keeps infinities out of the remainder
+    } else if (slot < 0 || bad_slot || bad_pos) {   // the group's
+      if (more) look_ahead(unit + stride);
+    } else {
+    uint8_t* rec = a.pool.record(slot, j0);
+    const long row_in = a.pool.row(slot);
+    if constexpr (TO == kToBf16Pages) {
+      rec += ((is_v ? a.pool.page_size : 0) + row_in) * a.hd * 2;
+#pragma unroll 1
+      for (int u = 0; u < jn; ++u, rec += a.pool.record_bytes) {
+        uint4 o0, o1;
+        advance(u, o0, o1);
+        if (!is_v) norm_rotate(o0, o1);
+        if (has0) *reinterpret_cast<uint4*>(rec + p0 * 16) = o0;
+        if (has1) *reinterpret_cast<uint4*>(rec + p1 * 16) = o1;
+      }
+    }
+    if constexpr (TO == kToFp4Pages) {
+      const float rk = __frcp_rn(static_scale);
+      const uint64_t rk2 = f2_pack(rk, rk);
+      rec += is_v ? a.pool.record_bytes / 2 : 0;
+      const long scales = long(a.pool.page_size) * (a.hd / 2) + row_in * (a.hd / 16);
+      // a block of 16 is two neighbouring pieces: who holds the other
+      int lane0, lane1, slot0, slot1;
+      at.find(p0 ^ 1, &lane0, &slot0);
+      at.find(p1 ^ 1, &lane1, &slot1);
+#pragma unroll 1
+      for (int u = 0; u < jn; ++u, rec += a.pool.record_bytes) {
+        uint4 o0, o1;
+        advance(u, o0, o1);
+        if (!is_v) norm_rotate(o0, o1);
+        uint64_t y[2][4];
+        unpack8_f2(o0, y[0]);  // what is cached is the bf16 key
+        unpack8_f2(o1, y[1]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          uint64_t& v = y[j / 4][j % 4];
-          v = f2_pack(fminf(fmaxf(f2_lo(v), -8192.0f), 8192.0f), fminf(fmaxf(f2_hi(v), -8192.0f), 8192.0f));
+        for (int j = 0; j < 4; ++j) {
+          y[0][j] = mul2(y[0][j], rk2);
+          y[1][j] = mul2(y[1][j], rk2);
         }
+        float big0 = absmax8(y[0]), big1 = absmax8(y[1]);
+        const float a0 = __shfl_sync(group, big0, lane0, LANES), a1 = __shfl_sync(group, big1, lane0, LANES);
+        const float b0 = __shfl_sync(group, big0, lane1, LANES), b1 = __shfl_sync(group, big1, lane1, LANES);
+        big0 = fmaxf(big0, slot0 ? a1 : a0);
+        big1 = fmaxf(big1, slot1 ? b1 : b0);
+        if (__any_sync(group, fmaxf(big0, big1) > 8192.0f)) {
+          // far past saturation: keeps infinities out of the remainder
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            uint64_t& v = y[j / 4][j % 4];
+            v = f2_pack(fminf(fmaxf(f2_lo(v), -8192.0f), 8192.0f), fminf(fmaxf(f2_hi(v), -8192.0f), 8192.0f));
+          }
+        }
+        const uint8_t s0 = block_scale(big0), s1 = block_scale(big1);
+        uint8_t* codes = rec + row_in * (a.hd / 2);
+        if (has0) *reinterpret_cast<uint32_t*>(codes + p0 * 4) = quantise8(y[0], s0);
+        if (has1) *reinterpret_cast<uint32_t*>(codes + p1 * 4) = quantise8(y[1], s1);
+        if (has0 && (p0 & 1) == 0) rec[scales + p0 / 2] = s0;
+        if (has1 && (p1 & 1) == 0) rec[scales + p1 / 2] = s1;
       }
-      const uint8_t s0 = block_scale(big0), s1 = block_scale(big1);
-      uint8_t* codes = rec + row_in * (a.hd / 2);
-      if (has0) *reinterpret_cast<uint32_t*>(codes + p0 * 4) = quantise8(y[0], s0);
-      if (has1) *reinterpret_cast<uint32_t*>(codes + p1 * 4) = quantise8(y[1], s1);
-      if (has0 && (p0 & 1) == 0) rec[scales + p0 / 2] = s0;
-      if (has1 && (p1 & 1) == 0) rec[scales + p1 / 2] = s1;
     }
+    }
+    if (!more) break;
+    unit += stride;
   }
 }
 
@@ -374,9 +400,10 @@ template <int LANES, int U>
 int launch_heads(int to, HeadArgs a, cudaStream_t s) {
   a.q_units = to == kToRows || a.q_out ? (a.hq + U - 1) / U : 0;
   const long units = long(a.rows) * (a.q_units + (a.hkv + U - 1) / U * (to == kToRows ? 1 : 2));
-  const long blocks = (units * LANES + 255) / 256;
   FRT_REQUIRE(units <= 0x7fffff00L, FRT_ESHAPE, "rows * heads is too large");
-  const dim3 grid{unsigned(blocks)}, block{256};
+  const long blocks = (units * LANES + 255) / 256, most = num_sms() * 2L;
+  const bool resident = to != kToRows;   // blocks that go from unit to unit
+  const dim3 grid{unsigned(resident && blocks > most ? most : blocks)}, block{256};
   switch (to) {
     case kToRows: return launch_pdl("frt_qk_norm_rope", head_kernel<LANES, U, kToRows>, grid, block, 0, s, a);
     case kToBf16Pages: return launch_pdl("frt_paged_kv_append", head_kernel<LANES, U, kToBf16Pages>, grid, block, 0, s, a);
