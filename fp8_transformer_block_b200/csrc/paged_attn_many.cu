@@ -14,6 +14,11 @@
 // hd 128 takes 2 x 512 clocks of MMA and 1024 of the 16-a-clock exponential
 // unit.  The widening of the codes is shared by all R rows (about a tenth of
 // the issue slots at R = 256), which is what the second row tile is for.
+// Neither is reached: a causal prompt of 8192 tokens, 32 q heads on 8 of 128,
+// runs in 586 to 611 us (about 940 TFLOP/s), because a row tile's chain, S to
+// P 2150 clocks and P to the next S 1980, is longer than the pipes' shares.
+// Tiles of 64 keys with Q K^T one ahead (831 us) and two threads a row (585)
+// did not shorten it.
 //
 // When the units (sequences x heads x row tiles) leave SMs idle, the keys of
 // each are cut into `splits`, whose partial states a second kernel joins.
