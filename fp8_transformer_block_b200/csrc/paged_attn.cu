@@ -888,7 +888,9 @@ extern "C" int frt_paged_attention_fp4(const frt_paged_attn_desc* d, void* strea
               d->workspace_bytes, need);
   frt::AttnArgs a{};
   a.n_seqs = d->n_seqs; a.rows = d->rows; a.max_q = d->max_q; a.hq = d->hq; a.hkv = d->hkv;
-  a.group = d->hq / d->hkv; a.causal = d->causal != 0; a.window = d->window;
+  a.group = d->hq / d->hkv; a.causal = d->causal != 0;
+  // no table holds more than 2^30 keys; place - window then stays in 32 bits
+  a.window = d->window < 0x40000000 ? d->window : 0x40000000;
   a.max_pages = d->max_pages; a.sm_scale = d->sm_scale;
   a.q = d->q; a.ld_q = d->ld_q;
   a.pool = frt::make_page_pool(const_cast<void*>(d->pool), FRT_PAGE_E2M1, d->page_size, d->n_pages,

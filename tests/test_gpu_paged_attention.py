@@ -188,6 +188,16 @@ def test_peaked_and_far_scores(rt):
         p.check()
 
 
+@pytest.mark.parametrize("window", [2 ** 30, 2 ** 31 - 40, 2 ** 31 - 1])
+@pytest.mark.parametrize("Lq", [6, 300])
+def test_windows_past_every_key(rt, Lq, window):
+    """The largest windows hide nothing, also where a tile's first queries
+    stand before the first key."""
+    p = Problem(rt, np.random.default_rng(21), [(Lq, 5), (Lq, 200), (1, 77)], 8, 2, 64, 16, window=window)
+    p.run()
+    p.check()
+
+
 @pytest.mark.parametrize("Lq", [1, 60])
 def test_scale_of_zero(rt, Lq):
     """Every visible key weighs the same."""
