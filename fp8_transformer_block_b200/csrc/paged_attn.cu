@@ -9,6 +9,7 @@
 // bits, 2^-10 .. 2688), so the cache is widened in registers to fp16 and the
 // products run on the tensor cores with fp32 sums; the static scales are
 // applied to the fp32 results.
+#include <cmath>
 #include <mutex>
 #include <set>
 #include <utility>
@@ -866,6 +867,7 @@ extern "C" int frt_paged_attention_fp4(const frt_paged_attn_desc* d, void* strea
               FRT_ESHAPE, "bad max_pages / n_pages: %d, %d", d->max_pages, d->n_pages);
   FRT_REQUIRE(d->window >= 0 && (d->window == 0 || d->causal), FRT_EINVAL,
               "a window must be >= 0 and needs causal");
+  FRT_REQUIRE(std::isfinite(d->sm_scale), FRT_EINVAL, "sm_scale must be finite");
   if (d->n_seqs == 0 || d->rows == 0 || d->max_q == 0) return FRT_OK;
   FRT_REQUIRE(d->q && d->out && d->kv_len && d->k_scale && d->v_scale, FRT_EINVAL,
               "q, out, kv_len, k_scale and v_scale are required");

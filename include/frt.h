@@ -600,7 +600,7 @@ typedef struct frt_paged_attn_desc {
   int hq, hkv, hd;        /* hq a multiple of hkv; hd 64, 128 or 256        */
   int page_size, max_pages, n_pages;
   int causal, window;     /* window > 0: causal, the last `window` keys     */
-  float sm_scale;
+  float sm_scale;         /* finite, of either sign                         */
   const frt_bf16* q; long ld_q;       /* [rows, hq * hd], strided           */
   const void* pool;       /* FRT_PAGE_E2M1 pool, 16-byte aligned            */
   const int* page_table;  /* device [n_seqs, max_pages]                     */

@@ -109,6 +109,7 @@ def test_read_refusals(frt, rt, change, code):
     (dict(page_table=None), -1), (dict(q=A16 + 8), -3), (dict(pool=A16 + 8), -3), (dict(ld_q=516), -3),
     (dict(ld_q=504), -2), (dict(ld_out=504), -2), (dict(cu_rows=A16 + 2), -3), (dict(lse=A16 + 1), -3),
     (dict(workspace=None), -1), (dict(workspace=A16 + 4), -3), (dict(workspace_bytes=16), -4),
+    (dict(sm_scale=float("nan")), -1), (dict(sm_scale=float("inf")), -1),
     (dict(n_seqs=0), 0), (dict(rows=0), 0), (dict(max_q=0), 0)])
 def test_attention_refusals(frt, rt, change, code):
     a = dict(n_seqs=3, rows=3, max_q=1, hq=8, hkv=2, hd=64, page_size=16, max_pages=8, n_pages=24, causal=1,
