@@ -110,7 +110,7 @@ __device__ __forceinline__ void lds(const uint8_t* p, uint32_t (&w)[BYTES / 4]) 
 // and the last of its CTAs to finish joins them in order.
 //
 // 61 sequences of one token and 700 to 16384 keys, 32 q heads on 8 of 128, run
-// in 131 to 138 us (93 for the bytes); what is between is the widening, 331
+// in 131 to 139 us (93 for the bytes); what is between is the widening, 331
 // warp instructions for 16 keys of a kv head.  Two groups of 16 keys a warp at
 // once hide its latency (one: 154 us), three CTAs an SM (four, with fewer
 // registers: 180).

@@ -15,7 +15,7 @@
 // unit.  The widening of the codes is shared by all R rows (about a tenth of
 // the issue slots at R = 256), which is what the second row tile is for.
 // Neither is reached: a causal prompt of 8192 tokens, 32 q heads on 8 of 128,
-// runs in 586 to 611 us (about 940 TFLOP/s), because a row tile's chain, S to
+// runs in 591 to 611 us (900 to 930 TFLOP/s), because a row tile's chain, S to
 // P 2150 clocks and P to the next S 1980, is longer than the pipes' shares.
 // Tiles of 64 keys with Q K^T one ahead (831 us) and two threads a row (585)
 // did not shorten it.
