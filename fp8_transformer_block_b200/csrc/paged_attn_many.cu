@@ -414,8 +414,8 @@ attn_many_kernel(AttnArgs a, int splits, int tiles_max) {
       mbar_arrive(&p_full[slot]);
     }
 
-    // --- the row's result: through shared memory (every buffer is idle
-    // now), so that the stores are whole rows ---
+    // --- the row's result: through shared memory (after `done` every buffer
+    // is idle), so that the stores are whole rows ---
     const float l = f2_lo(l2) + f2_hi(l2);
     const bool whole = splits == 1;
     float* part = partial_tile<HD>(a.partials, part_index);
@@ -561,7 +561,9 @@ attn_many_kernel(AttnArgs a, int splits, int tiles_max) {
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
       k[t] = 0;
-      if (n > 0) ok = ok && wait(&q_full[t], 0);
+      // without a key tile too: `done` lets the softmax warps stage results
+      // where other warps' rows of Q may still be on their way
+      ok = ok && wait(&q_full[t], 0);
     }
     if constexpr (QT == 2) {
       // at tile j, for each row tile: P V of tile j - 1 (its P overlies the
