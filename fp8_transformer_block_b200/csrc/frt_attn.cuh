@@ -12,8 +12,10 @@ namespace frt {
 constexpr uint64_t kAttnWaitNs = 2000000000ull;  // 2 s per wait
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-// stands for a score scale of 0, so that a hidden score (-inf) stays hidden
-constexpr float kTinyScale = 1e-30f;
+// The least factor from a row's products to its base-2 scores, so that a
+// hidden score (-inf) stays hidden: where the scale, or its product with the
+// row's power of two, is below it, scores are within 2^-100 of 0 either way.
+constexpr float kLeastFactor = 1.17549435e-38f;
 // the running maximum of a row that has seen no key
 constexpr float kNoKey = -1e30f;
 // Weights are 2^(score - m) and go to the tensor cores in fp16.  m is set to

@@ -333,7 +333,7 @@ attn_few_kernel(AttnArgs a) {
   // the sign of the scale goes into Q, so that the largest score is that of
   // the largest product
   const float scale = *a.k_scale * a.sm_scale * kLog2e;
-  const float kscale = scale == 0.0f ? kTinyScale : fabsf(scale);
+  const float kscale = fabsf(scale);
   const float vscale = *a.v_scale;
   // where in a stage this lane's bytes of the warp's first group lie, and
   // the way to the next group (in the next record's piece, if that is 16 keys)
@@ -412,7 +412,7 @@ attn_few_kernel(AttnArgs a) {
       } else {
 #pragma unroll
         for (int e2 = 0; e2 < 2; ++e2)
-          cq[nt][e2] = __shfl_sync(0xffffffffu, up, (2 * t + e2) * 4) * kscale;
+          cq[nt][e2] = fmaxf(__shfl_sync(0xffffffffu, up, (2 * t + e2) * 4) * kscale, kLeastFactor);
       }
     }
     if constexpr (!C::kQRegs) {
@@ -420,7 +420,7 @@ attn_few_kernel(AttnArgs a) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e2 = 0; e2 < 2; ++e2) cq[nt][e2] = join_m[nt * 8 + 2 * t + e2] * kscale;
+        for (int e2 = 0; e2 < 2; ++e2) cq[nt][e2] = fmaxf(join_m[nt * 8 + 2 * t + e2] * kscale, kLeastFactor);
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)

@@ -302,7 +302,7 @@ attn_many_kernel(AttnArgs a, int splits, int tiles_max) {
     // the sign of the scale goes into Q, so that the largest score is that of
     // the largest product
     const float down = copysignf(__uint_as_float(uint32_t(254 - e) << 23), scale);
-    const float c = (scale == 0.0f ? kTinyScale : fabsf(scale)) * __uint_as_float(uint32_t(e) << 23);
+    const float c = fmaxf(fabsf(scale) * __uint_as_float(uint32_t(e) << 23), kLeastFactor);
 #pragma unroll 4
     for (int i = 0; i < HD / 8; ++i) {
       float f[8];

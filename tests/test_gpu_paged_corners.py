@@ -36,3 +36,15 @@ def test_blocks_without_a_key_tile(rt, hd, hq, hkv, lens, causal):  # noqa: F811
     p.run()
     p.check()
     repeat(p, 10)
+
+
+@pytest.mark.parametrize("Lq", [1, 3, 60])
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("gain,scale", [(2.0 ** -80, 0.0), (2.0 ** -126, 0.0), (2.0 ** 100, 0.0), (2.0 ** 120, 0.0),
+                                        (2.0 ** -100, 1e-30), (2.0 ** -110, -1e-37), (1.0, 1e-45)])
+def test_factors_below_fp32(rt, Lq, hd, gain, scale):  # noqa: F811
+    """Scale times |q| from nothing to below the least fp32 number, under a
+    mask: every visible key weighs the same."""
+    p = Problem(rt, np.random.default_rng(32), [(Lq, 150), (1, 70), (Lq, 1)], 4, 2, hd, 16, scale=scale, q_gain=gain)
+    p.run()
+    p.check()
