@@ -23,6 +23,14 @@ constexpr float kNoKey = -1e30f;
 // kGrow: weights stay below 2^15, and those down to 2^-21 of the largest keep
 // all eleven bits (the least step is 2^-31 of it).
 constexpr float kLift = 7.0f, kGrow = 15.0f;
+// A weight's exponent is one fused multiply-add, factor * product - m, which
+// keeps what a rounded m cannot hold of the largest score: up to 2^-24 of it.
+// Products are below 2 * 2688 a term; a row whose factor could take them past
+// scores of 2^22 has the rounded scores in their place, and a factor of 1.
+template <int HD>
+__device__ __forceinline__ bool is_far(float factor) {
+  return factor > 4194304.0f / (HD * 5376);
+}
 
 struct AttnArgs {
   int n_seqs, rows, max_q, hq, hkv, group, causal, window;

@@ -333,7 +333,7 @@ attn_few_kernel(AttnArgs a) {
   // the sign of the scale goes into Q, so that the largest score is that of
   // the largest product
   const float scale = *a.k_scale * a.sm_scale * kLog2e;
-  const float kscale = fabsf(scale);
+  auto factor_of = [&](float up) { return fmaxf(up * fabsf(scale), kLeastFactor); };
   const float vscale = *a.v_scale;
   // where in a stage this lane's bytes of the warp's first group lie, and
   // the way to the next group (in the next record's piece, if that is 16 keys)
@@ -412,7 +412,7 @@ attn_few_kernel(AttnArgs a) {
       } else {
 #pragma unroll
         for (int e2 = 0; e2 < 2; ++e2)
-          cq[nt][e2] = fmaxf(__shfl_sync(0xffffffffu, up, (2 * t + e2) * 4) * kscale, kLeastFactor);
+          cq[nt][e2] = factor_of(__shfl_sync(0xffffffffu, up, (2 * t + e2) * 4));
       }
     }
     if constexpr (!C::kQRegs) {
@@ -420,7 +420,7 @@ attn_few_kernel(AttnArgs a) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e2 = 0; e2 < 2; ++e2) cq[nt][e2] = fmaxf(join_m[nt * 8 + 2 * t + e2] * kscale, kLeastFactor);
+        for (int e2 = 0; e2 < 2; ++e2) cq[nt][e2] = factor_of(join_m[nt * 8 + 2 * t + e2]);
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -449,6 +449,19 @@ attn_few_kernel(AttnArgs a) {
       all_hi = min(all_hi, __shfl_xor_sync(0xffffffffu, all_hi, o));
       all_lo = max(all_lo, __shfl_xor_sync(0xffffffffu, all_lo, o));
     }
+    bool far = false;   // of any of the warp's rows
+    float true_cq[C::kQRegs ? NT : 1][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e2 = 0; e2 < 2; ++e2) {
+        if constexpr (C::kQRegs) true_cq[nt][e2] = cq[nt][e2];
+        if (is_far<HD>(cq[nt][e2])) {
+          far = true;
+          cq[nt][e2] = 1.0f;
+        }
+      }
+    far = __any_sync(0xffffffffu, far);
     float o_acc[NT][HD / 16][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -468,7 +481,7 @@ attn_few_kernel(AttnArgs a) {
       if (__all_sync(0xffffffffu, got) && key0 < tile_hi && key0 + 16 * GR > tile_lo) {
         const uint8_t* st = ring + stage * C::kStage;
         const uint32_t have = valid[stage];
-        bool hidden[GR], masked = key0 + 16 * GR > all_hi || key0 < all_lo;
+        bool hidden[GR], masked = far || key0 + 16 * GR > all_hi || key0 < all_lo;
 #pragma unroll
         for (int u = 0; u < GR; ++u) {  // in a bad page
           hidden[u] = !(have >> piece[u] & 1);
@@ -531,6 +544,21 @@ attn_few_kernel(AttnArgs a) {
         // passes it by more than kGrow, so most groups pass without the
         // reduction
         if (masked) {
+          if (far) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e2 = 0; e2 < 2; ++e2) {
+                const float v = C::kQRegs ? true_cq[C::kQRegs ? nt : 0][e2]
+                                          : factor_of(join_m[nt * 8 + 2 * t + e2]);
+                const float f = is_far<HD>(v) ? v : 1.0f;
+#pragma unroll
+                for (int u = 0; u < GR; ++u) {
+                  s[u][nt][e2] = __fmul_rn(s[u][nt][e2], f);
+                  s[u][nt][e2 + 2] = __fmul_rn(s[u][nt][e2 + 2], f);
+                }
+              }
+          }
 #pragma unroll
           for (int u = 0; u < GR; ++u)
 #pragma unroll

@@ -5,6 +5,7 @@ size, and bytes that no other test looks at."""
 import numpy as np
 import pytest
 
+from fp8_transformer_block_b200.synth import bf16_value
 from test_gpu_paged_attention import Problem, rt  # noqa: F401  (rt: the fixture)
 
 pytestmark = pytest.mark.gpu
@@ -48,3 +49,43 @@ def test_factors_below_fp32(rt, Lq, hd, gain, scale):  # noqa: F811
     p = Problem(rt, np.random.default_rng(32), [(Lq, 150), (1, 70), (Lq, 1)], 4, 2, hd, 16, scale=scale, q_gain=gain)
     p.run()
     p.check()
+
+
+def check_far(p):
+    """Where a row's largest score leads the next by more than the error of a
+    score, the row's result is that key's value; weights are rounded to fp16
+    once (2^-11), sums and the exponential add a few 2^-22."""
+    o, lse = p.results()
+    for s, (Lq, L) in enumerate(p.lens):
+        k, v = p.kv[s]
+        G = p.hq // p.hkv
+        q = bf16_value(p.q)[p.cu[s]:p.cu[s + 1], :p.hq * p.hd].astype(np.float64).reshape(Lq, p.hq, p.hd)
+        led = 0
+        for i in range(Lq):
+            for h in range(p.hq):
+                seen = L - Lq + i + 1
+                x = q[i, h] @ k[h // G][:seen].T * p.scale
+                size = (np.abs(q[i, h]) @ np.abs(k[h // G][:seen]).T * abs(p.scale)).max()
+                # hd products summed in fp32 (2^-23 a step, the tensor core
+                # truncates), the scaling, q's fp16 form (2^-25 of its largest)
+                err = (p.hd + 6) * 2.0 ** -23 * size + 2.0 ** -25 * np.abs(q[i, h]).max() * abs(p.scale) * \
+                    np.abs(k[h // G]).sum(1).max()
+                top = np.argsort(x)[::-1][:2]
+                assert abs(lse[p.cu[s] + i, h] - x[top[0]]) <= 2 * err + np.log(seen) + 2.0 ** -22 * abs(x[top[0]])
+                if seen == 1 or x[top[0]] - x[top[1]] > 2 * err + 64:
+                    led += 1
+                    want = v[h // G][top[0]]
+                    got = o[p.cu[s] + i, h * p.hd:(h + 1) * p.hd]
+                    assert np.all(np.abs(got - want) <= np.abs(want) * (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -18)), (s, i, h)
+        assert led * 2 > Lq * p.hq
+
+
+@pytest.mark.parametrize("Lq", [1, 60])
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("scale", [1e6, 1e8, -1e9, 1e13, -1e20, 1e27])
+def test_far_scores(rt, Lq, hd, scale):  # noqa: F811
+    """Scores whose rounding is many steps of the exponent: one key a row."""
+    p = Problem(rt, np.random.default_rng(33), [(Lq, 150), (1, 1), (Lq, Lq)], 4, 2, hd, 16, scale=scale)
+    p.run()
+    p.check()
+    check_far(p)
