@@ -16,8 +16,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 // hidden score (-inf) stays hidden: where the scale, or its product with the
 // row's power of two, is below it, scores are within 2^-100 of 0 either way.
 constexpr float kLeastFactor = 1.17549435e-38f;
-// the running maximum of a row that has seen no key
-constexpr float kNoKey = -1e30f;
+// the running maximum of a row that has seen no key: below every score, and
+// finite, so that a hidden score's distance to it is -inf
+constexpr float kNoKey = -3.402823466e38f;
 // Weights are 2^(score - m) and go to the tensor cores in fp16.  m is set to
 // the largest score so far less kLift, and again once a score passes m by
 // kGrow: weights stay below 2^15, and those down to 2^-21 of the largest keep

@@ -5,7 +5,7 @@ size, and bytes that no other test looks at."""
 import numpy as np
 import pytest
 
-from fp8_transformer_block_b200.synth import bf16_value
+from fp8_transformer_block_b200.synth import bf16_bits, bf16_value
 from test_gpu_paged_attention import Problem, rt  # noqa: F401  (rt: the fixture)
 
 pytestmark = pytest.mark.gpu
@@ -89,3 +89,33 @@ def test_far_scores(rt, Lq, hd, scale):  # noqa: F811
     p.run()
     p.check()
     check_far(p)
+
+
+@pytest.mark.parametrize("Lq", [1, 60])
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("scale", [1e30, -1e33, 1e35])
+def test_scores_of_fp32s_size(rt, Lq, hd, scale):  # noqa: F811
+    """A row whose every score lies far below zero still sees its keys."""
+    p = Problem(rt, np.random.default_rng(33), [(Lq, 150), (1, 1), (Lq, Lq)], 4, 2, hd, 16, scale=scale)
+    p.run()
+    p.check()
+    check_far(p)
+
+
+@pytest.mark.parametrize("hd,Lq", [(64, 1), (128, 1), (256, 1), (64, 3), (128, 3), (64, 60), (128, 60), (256, 60)])
+def test_rows_of_different_sizes(rt, hd, Lq):  # noqa: F811
+    """Rows of ordinary scores beside rows of far ones in the same tile."""
+    frt, runtime, torch = rt
+    p = Problem(rt, np.random.default_rng(37), [(Lq, 200), (Lq, 70)], 8, 2, hd, 16)
+    p.run()
+    want, lse = p.out.clone(), p.lse.clone()
+    rows = np.zeros(p.q.shape, bool)
+    for h in (1, 6):   # one head of each kv head, in every third row
+        rows[::3, h * hd:(h + 1) * hd] = True
+    p.q[rows] = bf16_bits(bf16_value(p.q)[rows] * np.float32(2.0 ** 90))
+    p.t["q"].copy_(runtime.bf16_dev(p.q))
+    p.run()
+    p.check()
+    keep = torch.from_numpy(~rows).cuda()[:, :8 * hd]
+    assert torch.equal(p.out[keep], want[keep])
+    assert torch.equal(p.lse[keep[:, ::hd]], lse[keep[:, ::hd]])
