@@ -485,7 +485,7 @@ attn_many_kernel(AttnArgs a, int splits, int tiles_max) {
       }
     }
     if (live && whole && a.lse)
-      a.lse[long(q.r0 + token) * a.hq + h] = m == -INFINITY ? m : (m + log2f(l)) * kLn2;
+      a.lse[long(q.r0 + token) * a.hq + h] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
     if (!whole) {
       part[R * HD + t * 128 + r] = m;
       part[R * HD + R + t * 128 + r] = l;
@@ -740,7 +740,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, int splits, 
 #pragma unroll
   for (int v = 0; v < V; v += 2) dst[v / 2 * 32 + lane] = pack_bf16x2(acc[v] * inv, acc[v + 1] * inv);
   if (lane == 0 && a.lse)
-    a.lse[long(q.r0 + token) * a.hq + h] = m == -INFINITY ? m : (m + log2f(l)) * kLn2;
+    a.lse[long(q.r0 + token) * a.hq + h] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 template <int HD>

@@ -119,3 +119,22 @@ def test_rows_of_different_sizes(rt, hd, Lq):  # noqa: F811
     keep = torch.from_numpy(~rows).cuda()[:, :8 * hd]
     assert torch.equal(p.out[keep], want[keep])
     assert torch.equal(p.lse[keep[:, ::hd]], lse[keep[:, ::hd]])
+
+
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("lens,hq,hkv", [
+    ([(1, 300)], 8, 2), ([(1, 9000)], 8, 2),     # few rows: a whole unit, a cut one
+    ([(50, 866)], 8, 1), ([(64, 300)] * 10, 32, 8)])  # many: split keys, whole
+def test_nan_in_q(rt, hd, lens, hq, hkv):  # noqa: F811
+    """A NaN stays in its row and head, in out and lse alike."""
+    torch = rt[2]
+    p = Problem(rt, np.random.default_rng(34), lens, hq, hkv, hd, 32)
+    p.run()
+    out, lse = p.out.clone(), p.lse.clone()
+    row, h = int(p.cu[-1]) - 1, hq - 1
+    at = slice(h * hd, (h + 1) * hd)
+    p.t["q"][row, h * hd + 5] = float("nan")
+    p.run()
+    assert bool(torch.isnan(p.out[row, at]).all()) and bool(torch.isnan(p.lse[row, h]))
+    p.out[row, at], p.lse[row, h] = out[row, at], lse[row, h]
+    assert torch.equal(p.out, out) and torch.equal(p.lse, lse)
