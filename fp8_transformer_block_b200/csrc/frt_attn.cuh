@@ -26,8 +26,9 @@ constexpr float kNoKey = -3.402823466e38f;
 constexpr float kLift = 7.0f, kGrow = 15.0f;
 // A weight's exponent is one fused multiply-add, factor * product - m, which
 // keeps what a rounded m cannot hold of the largest score: up to 2^-24 of it.
-// Products are below 2 * 2688 a term; a row whose factor could take them past
-// scores of 2^22 has the rounded scores in their place, and a factor of 1.
+// Products are below 2 * 2688 a term (twice that for |q| from 2^127 on); a row
+// whose factor could take them past scores of 2^22 has the rounded scores in
+// their place, and a factor of 1.
 template <int HD>
 __device__ __forceinline__ bool is_far(float factor) {
   return factor > 4194304.0f / (HD * 5376);
@@ -77,6 +78,13 @@ __device__ __forceinline__ Seq load_seq(const AttnArgs& a, int s, bool report) {
   q.chunk0 = int(first / CK);
   q.chunks = max(1, int((L + CK - 1) / CK) - q.chunk0);
   return q;
+}
+
+// The biased exponent of the power of two that a row of q is divided by: that
+// of its largest, as near as both the power and its inverse are normal numbers
+// (so a row is below 2, or below 4 from 2^127 on).
+__device__ __forceinline__ int q_exponent(float largest) {
+  return min(max(int(__float_as_uint(largest) >> 23), 1), 253);
 }
 
 __device__ __forceinline__ float ex2(float x) {

@@ -394,8 +394,7 @@ attn_few_kernel(AttnArgs a) {
                                fabsf(__uint_as_float(raw[i] & 0xFFFF0000u))));
       big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
       big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-      int e = int(__float_as_uint(big) >> 23);  // 2^(e - 127) <= big
-      if (e < 1 || e > 253) e = 127;            // zero, subnormal, infinite: as it is
+      const int e = q_exponent(big);
       const float down = copysignf(__uint_as_float(uint32_t(254 - e) << 23), scale);
       const float up = __uint_as_float(uint32_t(e) << 23);
 #pragma unroll

@@ -299,8 +299,7 @@ attn_many_kernel(AttnArgs a, int splits, int tiles_max) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) big = fmaxf(big, fabsf(f[k]));
     }
-    int e = int(__float_as_uint(big) >> 23);
-    if (e < 1 || e > 253) e = 127;
+    const int e = q_exponent(big);
     // the sign of the scale goes into Q, so that the largest score is that of
     // the largest product
     const float down = copysignf(__uint_as_float(uint32_t(254 - e) << 23), scale);

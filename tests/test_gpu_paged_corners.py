@@ -138,3 +138,17 @@ def test_nan_in_q(rt, hd, lens, hq, hkv):  # noqa: F811
     assert bool(torch.isnan(p.out[row, at]).all()) and bool(torch.isnan(p.lse[row, h]))
     p.out[row, at], p.lse[row, h] = out[row, at], lse[row, h]
     assert torch.equal(p.out, out) and torch.equal(p.lse, lse)
+
+
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("Lq", [1, 3, 60])
+@pytest.mark.parametrize("size,scale", [(2.0 ** 127, 2.0 ** -123), (2.0 ** -131, 3e38)])
+def test_q_at_the_ends_of_bf16(rt, hd, Lq, size, scale):  # noqa: F811
+    """Rows whose largest |q| is 2^127 and above, and subnormal rows."""
+    runtime = rt[1]
+    rng = np.random.default_rng(38)
+    p = Problem(rt, rng, [(Lq, 150), (1, 40)], 4, 2, hd, 16, scale=scale)
+    p.q = bf16_bits(rng.uniform(-1.9, 1.9, p.q.shape).astype(np.float32) * np.float32(size))
+    p.t["q"].copy_(runtime.bf16_dev(p.q))
+    p.run()
+    p.check()
