@@ -138,16 +138,17 @@ __device__ __forceinline__ uint8_t block_scale(float a) {
   return __nv_cvt_float_to_fp8(t, __NV_SATFINITE, __NV_E4M3);
 }
 
-// 8 elements y of a block with that scale to e2m1 codes.
-__device__ __forceinline__ uint32_t quantise8(const uint64_t (&y)[4], uint8_t s8) {
+// 8 elements of a block with that scale to e2m1 codes, from their negatives n:
+// the remainder q s + n and its product with -r then keep the sign of a zero.
+__device__ __forceinline__ uint32_t quantise8(const uint64_t (&n)[4], uint8_t s8) {
   const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw(s8, __NV_E4M3)));
   const float r = s == 0.0f ? 0.0f : __frcp_rn(s);   // scale 0: codes 0
-  const uint64_t r2 = f2_pack(r, r), ns2 = f2_pack(-s, -s);
+  const uint64_t nr2 = f2_pack(-r, -r), s2 = f2_pack(s, s);
   uint32_t w = 0;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const uint64_t q = mul2(y[j], r2);
-    const uint64_t t = fma2(fma2(q, ns2, y[j]), r2, q);
+    const uint64_t q = mul2(n[j], nr2);
+    const uint64_t t = fma2(fma2(q, s2, n[j]), nr2, q);
     w |= uint32_t(__nv_cvt_float2_to_fp4x2(make_float2(f2_lo(t), f2_hi(t)), __NV_E2M1,
                                            cudaRoundNearest)) << (8 * j);
   }
@@ -348,7 +349,7 @@ __global__ void __launch_bounds__(256, U == 1 || TO != kToRows ? 2 : 3) head_ker
       }
     }
     if constexpr (TO == kToFp4Pages) {
-      const float rk = __frcp_rn(static_scale);
+      const float rk = -__frcp_rn(static_scale);   // the negatives, for quantise8
       const uint64_t rk2 = f2_pack(rk, rk);
       rec += is_v ? a.pool.record_bytes / 2 : 0;
       const long scales = long(a.pool.page_size) * (a.hd / 2) + row_in * (a.hd / 16);

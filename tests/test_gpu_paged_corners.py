@@ -5,7 +5,9 @@ size, and bytes that no other test looks at."""
 import numpy as np
 import pytest
 
+import paged_ref as ref
 from fp8_transformer_block_b200.synth import bf16_bits, bf16_value
+from test_gpu_paged import page_fields, record_rows
 from test_gpu_paged_attention import Problem, rt  # noqa: F401  (rt: the fixture)
 
 pytestmark = pytest.mark.gpu
@@ -152,3 +154,29 @@ def test_q_at_the_ends_of_bf16(rt, hd, Lq, size, scale):  # noqa: F811
     p.t["q"].copy_(runtime.bf16_dev(p.q))
     p.run()
     p.check()
+
+
+@pytest.mark.parametrize("hd,hkv", [(64, 2), (208, 1), (256, 5)])
+def test_codes_of_zeros(rt, hd, hkv):  # noqa: F811
+    """The bytes of zeros of either sign, among others and alone, and of what
+    rounds to zero."""
+    frt, runtime, torch = rt
+    rng = np.random.default_rng(35)
+    rows, ps = 40, 16
+    x = rng.standard_normal((rows, 2 * hkv * hd), dtype=np.float32)
+    x[rng.random(x.shape) < 0.3] = -0.0
+    x[rng.random(x.shape) < 0.2] = 0.0
+    x[rng.random(x.shape) < 0.1] *= np.float32(2.0 ** -40)
+    x[3], x[4] = -0.0, np.where(rng.random(x.shape[1]) < 0.5, 0.0, -0.0)
+    bits = bf16_bits(x)
+    dev = runtime.bf16_dev(bits)
+    f, slots, pool, kv, keep = page_fields(rt, 1, rng, rows, hkv, hd, ps)
+    frt.frt_paged_kv_append(runtime.qk_rope_desc(
+        rows=rows, hq=0, hkv=hkv, hd=hd, rot=0, layout=0, eps=1e-6, qkv=dev, ld_qkv=x.shape[1], **f))
+    torch.cuda.synchronize()
+    got = record_rows(pool, 1, hkv, hd, ps, slots)
+    v = bf16_value(bits).reshape(rows, 2, hkv, hd)
+    for i, scale in enumerate((0.0017391147, 0.03125)):
+        codes, s8 = ref.quantise(v[:, i], scale)
+        assert np.array_equal(got[2 * i], ref.pack_codes(codes))
+        assert np.array_equal(got[2 * i + 1], s8.astype(np.uint8))
