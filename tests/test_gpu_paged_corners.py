@@ -180,3 +180,36 @@ def test_codes_of_zeros(rt, hd, hkv):  # noqa: F811
         codes, s8 = ref.quantise(v[:, i], scale)
         assert np.array_equal(got[2 * i], ref.pack_codes(codes))
         assert np.array_equal(got[2 * i + 1], s8.astype(np.uint8))
+
+
+def counters_are_zero(p):
+    """All of the workspace's head that a later call could find counters in."""
+    head = p.ws[:4096].view(p.rt[2].int32)
+    assert head.numel() == 1024 and int(head.abs().sum()) == 0
+
+
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("hq,hkv,Lq", [(8, 1, 1), (8, 2, 2), (16, 1, 1), (12, 1, 1), (8, 2, 4), (3, 1, 5), (32, 1, 1),
+                                       (4, 2, 15), (8, 1, 3)])
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 130)])
+def test_table_capacities(rt, hd, hq, hkv, Lq, causal, window):  # noqa: F811
+    """1 to 32 rows of a kv head over a table just wide enough and over a wide
+    one: 9 to 32 rows go to one kernel or the other by the table's width."""
+    for extra in (0, 80):
+        p = Problem(rt, np.random.default_rng(36), [(Lq, 1300), (Lq, 64), (1, 513), (Lq, Lq), (0, 90)], hq, hkv, hd, 64,
+                    causal, window, extra_pages=extra)
+        p.run()
+        p.check()
+        counters_are_zero(p)
+
+
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("hq,hkv", [(8, 1), (16, 1), (24, 1), (8, 8)])
+@pytest.mark.parametrize("lens", [[(1, 20000)], [(1, 5000), (1, 1), (1, 3333)] * 9])
+def test_cut_units_leave_counters_at_zero(rt, hd, hq, hkv, lens):  # noqa: F811
+    p = Problem(rt, np.random.default_rng(39), lens, hq, hkv, hd, 128)
+    p.run()
+    p.check()
+    counters_are_zero(p)
+    repeat(p, 3)
+    counters_are_zero(p)
