@@ -213,3 +213,85 @@ def test_cut_units_leave_counters_at_zero(rt, hd, hq, hkv, lens):  # noqa: F811
     counters_are_zero(p)
     repeat(p, 3)
     counters_are_zero(p)
+
+
+@pytest.mark.parametrize("Lq", [1, 5, 200])
+def test_rows_of_bad_row_offsets(rt, Lq):  # noqa: F811
+    """Row offsets that run backwards, past the tensor or past max_q: the
+    rows that are left of each sequence, and nothing else, are written."""
+    frt, runtime, torch = rt
+    p = Problem(rt, np.random.default_rng(40), [(Lq, 600), (Lq, 300)], 4, 1, 64, 64, causal=False)
+    q = bf16_value(p.q).astype(np.float64).reshape(p.rows, 4, 64)
+    for cu in ([0, Lq, 5 * Lq + 99], [-4, Lq, 2 * Lq], [0, Lq, 0], [2 ** 30, Lq, 2 * Lq], [0, 2 ** 31 - 1, 2 ** 31 - 1],
+               [-2 ** 31, -1, 2 * Lq], [Lq, 0, Lq], [p.rows, p.rows + 1, 0]):
+        p.t["cu_rows"].copy_(torch.tensor(cu, dtype=torch.int32))
+        p.out.fill_(5.0)
+        p.lse.fill_(5.0)
+        p.run(report=False)
+        assert frt.frt_device_status(True) == frt.FRT_ERANGE
+        o, lse = p.results()
+        left = np.ones(p.rows, bool)
+        for s in range(2):
+            lo = min(max(cu[s], 0), p.rows)
+            hi = min(max(cu[s + 1], lo), p.rows, lo + Lq)
+            if hi == lo:
+                continue
+            # no two of these ranges overlap
+            assert np.all(left[lo:hi])
+            left[lo:hi] = False
+            k, v = p.kv[s]
+            want, wl, tol, tl = ref.attention(q[lo:hi], k, v, p.lens[s][1], False, 0, p.scale)
+            got = o[lo:hi].reshape(want.shape)
+            assert np.all(np.abs(got - want) <= ref.HALF_BF16 * np.abs(want) + tol), (cu, s)
+            assert np.all(np.abs(lse[lo:hi] - wl) <= tl)
+        assert np.all(o[left] == 5.0) and np.all(lse[left] == 5.0), cu
+
+
+@pytest.mark.parametrize("ps", [16, 64, 1024])
+@pytest.mark.parametrize("lens", [[(1, 700), (1, 130)], [(5, 700), (2, 70)], [(70, 700), (3, 90)]])
+def test_attention_over_a_pool_past_32_bits(rt, lens, ps):  # noqa: F811
+    """Pages whose byte offsets pass 2^32, in every kernel's copies."""
+    frt, runtime, torch = rt
+    p = Problem(rt, np.random.default_rng(41), lens, 8, 2, 256, ps)
+    small = p.t["pool"]
+    n_pages = (5 << 30) // small[0].numel()
+    pool = torch.empty(n_pages, *small.shape[1:], dtype=torch.uint8, device="cuda")
+    pool[n_pages - p.n_pages:] = small.flip(0)
+    table = torch.from_numpy(np.where(p.table >= 0, n_pages - 1 - p.table, p.table))
+    p.t["page_table"].copy_(table)
+    p.d.pool, p.d.n_pages = frt.ptr(pool), n_pages
+    p.run()
+    p.check()
+
+
+def test_keys_past_32_bits(rt):  # noqa: F811
+    """Appended and read back where slots' byte offsets pass 2^32, keys and
+    values alike, in both formats."""
+    frt, runtime, torch = rt
+    hkv, hd, ps, rows = 2, 256, 1024, 40
+    rng = np.random.default_rng(42)
+    x = bf16_bits(rng.standard_normal((rows, 2 * hkv * hd), dtype=np.float32))
+    dev = runtime.bf16_dev(x)
+    v = bf16_value(x).reshape(rows, 2, hkv, hd)
+    scale = runtime.scale_dev(0.25)
+    for fmt in (0, 1):
+        rec = frt.frt_kv_record_bytes(fmt, ps, hd)
+        n_pages = (9 << 30) // (hkv * rec)
+        pool = torch.empty(n_pages, hkv, rec, dtype=torch.uint8, device="cuda")
+        slots = torch.tensor([n_pages * ps - 1 - 7 * i for i in range(rows)], device="cuda")
+        kv = [torch.zeros(rows, hkv * hd, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        d = runtime.qk_rope_desc(
+            rows=rows, hq=0, hkv=hkv, hd=hd, rot=0, layout=0, eps=1e-6, qkv=dev, ld_qkv=x.shape[1], format=fmt,
+            page_size=ps, n_pages=n_pages, pool=pool, slots=slots, k_scale=scale, v_scale=scale, k_out=kv[0],
+            ld_k=hkv * hd, v_out=kv[1], ld_v=hkv * hd)
+        frt.frt_paged_kv_append(d)
+        frt.frt_paged_kv_read(d)
+        torch.cuda.synchronize()
+        assert frt.frt_device_status(True) == frt.FRT_OK
+        for i in range(2):
+            want = v[:, i]
+            if fmt == 1:
+                codes, s8 = ref.quantise(want, 0.25)
+                want = ref.E2M1[codes] * np.repeat(ref.E4M3[s8], 16, -1) * 0.25
+            assert np.array_equal(bf16_value(runtime.bf16_host(kv[i])).reshape(want.shape), want)
+        del pool
