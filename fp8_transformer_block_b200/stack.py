@@ -43,7 +43,9 @@ class AdaRmsLayerStack:
         then computes all norms' rows on the device (`fin` is unused).
         attention: None (the stand-in), or "paged_fp4" (each layer's keys and
         values, prefix included, in 4-bit pages of 16 tokens; their static
-        scales are calibrated with the others, or given as a_k and a_v)."""
+        scales are calibrated with the others, or given as a_k and a_v).  The
+        stand-in's steps copy the prefix into the caches each time; in pages
+        it is laid down here and by load_prefix."""
         assert w.hq * w.hd == w.D, "the attention output needs hq * hd == D"
         assert attention in (None, "paged_fp4"), attention
         self.w = w
@@ -262,6 +264,20 @@ class AdaRmsLayerStack:
     def load(self, x):
         """Set the stack's input rows (bf16 bits [rows, D])."""
         self.res.copy_(rt.bf16_dev(x))
+
+    def load_prefix(self, prefix):
+        """Set every layer's prefix: per layer (keys, values), bf16 bits
+        [B, hkv, P, hd] like the layers' prefix_k and prefix_v.  Steps and
+        graphs captured before read the new one.  The static scales stay:
+        in 4-bit pages what passes the scales' range saturates."""
+        assert self.w.P and len(prefix) == self.L, "one (keys, values) pair per layer with a prefix"
+        for l, (k, v) in enumerate(prefix):
+            for name, x in (("pk", k), ("pv", v)):
+                x = rt.bf16_dev(x)
+                assert x.shape == self.lay[l][name].shape, x.shape
+                self.lay[l][name].copy_(x)
+            if self.att:
+                self._load_prefix(l, self.scales[l]["a_k"], self.scales[l]["a_v"])
 
     # ------------------------------------------------------------------
     def calibrate(self, x):

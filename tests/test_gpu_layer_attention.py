@@ -110,3 +110,46 @@ def test_unknown_attention_is_refused(rt):
     layers = [synth.full_layer_inputs(w, l) for l in range(w.layers)]
     with pytest.raises(AssertionError):
         stack.AdaRmsLayerStack(w, layers, synth.final_norm_rows(w), x=None, attention="dense")
+
+
+@pytest.mark.parametrize("attention", [None, "paged_fp4"])
+def test_a_changed_prefix_changes_the_result(rt, attention):
+    """load_prefix, eagerly and under a captured step, against a stack built
+    with that prefix."""
+    frt, runtime, stack, torch = rt
+    w = workload(2, 20, 37, 2, 64)
+    layers = [synth.full_layer_inputs(w, l) for l in range(w.layers)]
+    x = synth.adarms_inputs(w.rows, w.D, w.seed)["res"]
+    fin = synth.final_norm_rows(w)
+    st = stack.AdaRmsLayerStack(w, layers, fin, x=x, attention=attention)
+    changed = []
+    for l, ly in enumerate(layers):
+        k, v = np.asarray(ly["prefix_k"]), np.asarray(ly["prefix_v"])
+        # other tokens of the same sizes: turned around, signs changed
+        changed.append(dict(ly, prefix_k=np.ascontiguousarray(k[:, :, ::-1]) ^ 0x8000,
+                            prefix_v=np.ascontiguousarray(v[:, :, ::-1])))
+    other = stack.AdaRmsLayerStack(w, changed, fin, scales=st.scales, attention=attention)
+
+    def result(run, s):
+        s.load(x)
+        run()
+        torch.cuda.synchronize()
+        return [s.out.clone()] + [s.lay[l][c][:, :w.P].clone() for l in range(w.layers) for c in ("kc", "vc")]
+
+    first, want = result(st.step, st), result(other.step, other)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        st.step()
+    st.load_prefix([(ly["prefix_k"], ly["prefix_v"]) for ly in changed])
+    for run in (st.step, graph.replay):
+        got = result(run, st)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        # the stand-in's result does not hang on the prefix, its caches do
+        assert not torch.equal(got[1], first[1])
+        assert torch.equal(got[0], first[0]) == (attention is None)
+    st.load_prefix([(ly["prefix_k"], ly["prefix_v"]) for ly in layers])
+    assert all(torch.equal(a, b) for a, b in zip(result(graph.replay, st), first))
+    with pytest.raises(AssertionError):
+        st.load_prefix([(changed[0]["prefix_k"], changed[0]["prefix_v"])])
+    with pytest.raises(AssertionError):
+        st.load_prefix([(ly["prefix_k"][:, :, 1:], ly["prefix_v"]) for ly in layers])
