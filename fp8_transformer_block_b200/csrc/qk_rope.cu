@@ -495,10 +495,10 @@ int check_rows(const char* name, const void* p, long ld, long width) {
   return FRT_OK;
 }
 
-int check_heads(const frt_qk_rope_desc* d) {
-  FRT_REQUIRE(d, FRT_EINVAL, "descriptor is NULL");
-  FRT_REQUIRE(d->rows >= 0 && d->hq >= 0 && d->hkv >= 0 && d->hq <= 65536 && d->hkv <= 65536,
-              FRT_ESHAPE, "bad rows / heads: %d, %d, %d", d->rows, d->hq, d->hkv);
+// hq: the descriptor's, or 0 where the call has no q heads
+int check_heads(const frt_qk_rope_desc* d, int hq) {
+  FRT_REQUIRE(d->rows >= 0 && hq >= 0 && d->hkv >= 0 && hq <= 65536 && d->hkv <= 65536,
+              FRT_ESHAPE, "bad rows / heads: %d, %d, %d", d->rows, hq, d->hkv);
   FRT_REQUIRE(d->hd >= 16 && d->hd <= 256 && d->hd % 8 == 0, FRT_ESHAPE,
               "hd must be a multiple of 8 in [16, 256], got %d", d->hd);
   return FRT_OK;
@@ -612,7 +612,8 @@ extern "C" size_t frt_kv_record_bytes(int format, int page_size, int hd) {
 
 extern "C" int frt_qk_norm_rope(const frt_qk_rope_desc* d, void* stream) {
   frt::clear_error();
-  if (int rc = frt::check_heads(d)) return rc;
+  FRT_REQUIRE(d, FRT_EINVAL, "descriptor is NULL");
+  if (int rc = frt::check_heads(d, d->hq)) return rc;
   if (int rc = frt::check_rotation(d)) return rc;
   FRT_REQUIRE(d->hq + d->hkv >= 1, FRT_ESHAPE, "there are no heads");
   if (d->rows == 0) return FRT_OK;
@@ -630,7 +631,8 @@ extern "C" int frt_qk_norm_rope(const frt_qk_rope_desc* d, void* stream) {
 
 extern "C" int frt_paged_kv_append(const frt_qk_rope_desc* d, void* stream) {
   frt::clear_error();
-  if (int rc = frt::check_heads(d)) return rc;
+  FRT_REQUIRE(d, FRT_EINVAL, "descriptor is NULL");
+  if (int rc = frt::check_heads(d, d->hq)) return rc;
   if (int rc = frt::check_rotation(d)) return rc;
   if (d->rows == 0) return FRT_OK;
   if (int rc = frt::check_pool(d)) return rc;
@@ -647,7 +649,8 @@ extern "C" int frt_paged_kv_append(const frt_qk_rope_desc* d, void* stream) {
 
 extern "C" int frt_paged_kv_read(const frt_qk_rope_desc* d, void* stream) {
   frt::clear_error();
-  if (int rc = frt::check_heads(d)) return rc;
+  FRT_REQUIRE(d, FRT_EINVAL, "descriptor is NULL");
+  if (int rc = frt::check_heads(d, 0)) return rc;
   if (d->rows == 0) return FRT_OK;
   if (int rc = frt::check_pool(d)) return rc;
   FRT_REQUIRE(d->k_out || d->v_out, FRT_EINVAL, "k_out or v_out is required");

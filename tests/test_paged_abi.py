@@ -132,3 +132,13 @@ def test_workspace_size(frt):
     assert frt.frt_paged_attention_workspace_size(4, 1, 8, 3, 128) == 0
     assert frt.frt_paged_attention_workspace_size(4, 1, 8, 1, 96) == 0
     assert frt.frt_paged_attention_workspace_size(-1, 1, 8, 1, 64) == 0
+
+
+@pytest.mark.parametrize("unused", [dict(hq=-1), dict(hq=1 << 20), dict(rot=7, layout=9, eps=-1.0, n_pos=-1, rope=A16 + 2),
+                                    dict(qkv=None, ld_qkv=3, q_out=A16 + 2, ld_q=1, q_norm=A16 + 2)])
+def test_read_does_not_look_at_other_fields(frt, rt, unused):
+    """frt_paged_kv_read uses rows, hkv, hd, k_out, v_out and the page fields
+    only: nothing else is a reason to refuse (rows = 0 ends ahead of the
+    device)."""
+    assert frt.raw_call("frt_paged_kv_read", C.byref(_heads(rt, rows=0, **unused)), None) == 0
+    assert frt.raw_call("frt_paged_kv_read", C.byref(_heads(rt, page_size=24, **unused)), None) == -2
