@@ -110,10 +110,13 @@ __device__ __forceinline__ void lds(const uint8_t* p, uint32_t (&w)[BYTES / 4]) 
 // and the last of its CTAs to finish joins them in order.
 //
 // 61 sequences of one token and 700 to 16384 keys, 32 q heads on 8 of 128, run
-// in 131 to 139 us (93 for the bytes); what is between is the widening, 331
-// warp instructions for 16 keys of a kv head.  Two groups of 16 keys a warp at
-// once hide its latency (one: 154 us), three CTAs an SM (four, with fewer
-// registers: 180).
+// in 133 us (93 for the bytes).  No unit is full: on 24 sequences of 8500 keys
+// 56 % of the issue slots and 3.6 TB/s.  The 12 computing warps of an SM have
+// a chain each from the widening (most of the 331 warp instructions for 16
+// keys of a kv head) over the products and the softmax to the next widening,
+// and wait for fixed latencies first.  Two groups of 16 keys a warp at once
+// hide part of it (one: 154 us), three CTAs an SM (four, with fewer registers:
+// 180).
 
 template <int HD, int NT>
 struct FewCfg {
@@ -848,10 +851,21 @@ auto with_variant(int hd, long rows_per_head, F f) {
 
 // Which kernel takes the rows of one kv head.  Above 32 rows always the
 // tensor-memory one.  For 9 to 32 rows the register kernel streams the cache
-// faster (32 sequences of 700 to 8000 keys, 16 rows: 37 us against 110), but
-// where the units are few and the table short, the other's splits are done
-// sooner (3 sequences of 900 to 2000 keys, 2 kv heads: 16 rows 16.6 us
-// against 18.6, 32 rows 17.8 against 27.2): with 256 keys at most to a split.
+// faster, but where the units are few and the keys short, the other's splits
+// are done sooner.  Lengths are known on the device only, so the rule goes by
+// what the table could hold: 256 keys at most to a split.  Measured with 2 kv
+// heads, register kernel / tensor-memory kernel, us:
+//                                    hd 64        hd 128       hd 256
+//   3 sequences of    16 rows     14.7 / 13.9  18.2 / 16.4  26.4 / 20.2
+//   900 to 2000 keys  32 rows     23.6 / 15.0  27.6 / 17.8  27.2 / 22.0
+//   12 sequences of   16 rows     16.9 / 18.4  20.0 / 20.8  30.4 / 23.2
+//   500 to 1500 keys  32 rows     24.3 / 19.8  28.9 / 22.2  31.8 / 24.9
+//   32 sequences of   16 rows     25.3 / 98.4  36.0 / 113   75.5 / 110
+//   700 to 8000 keys  32 rows     40.9 / 99.8  66.6 / 120   127 / 108
+// With tables just wide enough the rule takes the second kernel for the first
+// two and the first for the third (not the faster one at 12 x 16 rows of 64
+// and 128, nor at 32 x 32 rows of 256).  A wide table over short sequences
+// takes the first.
 bool many_rows(long rows_per_head, long units, long keys) {
   if (rows_per_head > 32) return true;
   if (rows_per_head <= 8 || units > num_sms()) return false;

@@ -15,8 +15,9 @@
 // unit.  The widening of the codes is shared by all R rows (about a tenth of
 // the issue slots at R = 256), which is what the second row tile is for.
 // Neither is reached: a causal prompt of 8192 tokens, 32 q heads on 8 of 128,
-// runs in 591 to 611 us (900 to 930 TFLOP/s), because a row tile's chain, S to
-// P 2150 clocks and P to the next S 1980, is longer than the pipes' shares.
+// runs in 593 us on one input and 607 over changing ones (905 to 927 TFLOP/s),
+// because a row tile's chain, in an earlier build of 585 us S to P 2150 clocks
+// and P to the next S 1980, is longer than the pipes' shares.
 // Tiles of 64 keys with Q K^T one ahead (831 us) and two threads a row (585)
 // did not shorten it.
 //
@@ -212,9 +213,10 @@ attn_many_kernel(AttnArgs a, int splits, int tiles_max) {
     fence_barrier_init();
   }
   pdl_wait();
-  // ahead of the sequence's lookup, which hides it (a prompt of 8192 tokens 591
-  // us against 602, 32 sequences of 1 to 2048 tokens 2176 against 2212; a block
-  // without rows pays for it too: 4096 tokens among 63 of one, 916 against 888)
+  // ahead of the sequence's lookup, which hides it (when far rows had no loop
+  // of their own yet: a prompt of 8192 tokens 591 us against 602, 32 sequences
+  // of 1 to 2048 tokens 2176 against 2212; a block without rows pays for it
+  // too: 4096 tokens among 63 of one, 916 against 888)
   if (warp == 12) {
     tmem_alloc(tmem_ptr, C::kTmem);
     tmem_relinquish();
@@ -328,8 +330,9 @@ attn_many_kernel(AttnArgs a, int splits, int tiles_max) {
     const float c = live && is_far<HD>(factor) ? 1.0f : factor;
     const uint64_t c2 = f2_pack(c, c);
     // Two loops: with the products of far rows in a branch of one loop, the
-    // expert's 50 tokens took 20.6 us for 19.5, a prompt of 8192 594 for 590
-    // (592 so), 32 sequences of 1 to 2048 tokens 2221 for 2140 (2190 so).
+    // expert's 50 tokens took 20.6 us (19.5 so and without far rows), a prompt
+    // of 8192 594 (592 so, 590 without), 32 sequences of 1 to 2048 tokens 2221
+    // (2190 so, 2140 without), 4096 tokens among 63 of one 937 so, 917 without.
     auto attend = [&](auto far) {
     for (int j = begin[t]; got_q && j < end[t]; ++j, ++k) {
       const int slot = QT == 2 ? t : k & 1;

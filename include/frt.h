@@ -500,8 +500,10 @@ enum {
  * 8-byte aligned (frt_qk_rope_desc.rope wants 16).  rot even, 2 <= rot <=
  * 65536; M, P >= 0; theta > 0; factor > 0, amplitude finite; rot > 2 for
  * FRT_ROPE_SCALE_BASE; orig_len > 0 and high_turns > low_turns for
- * FRT_ROPE_SCALE_PARTS (the three are ignored otherwise).  Within 1 ulp of
- * the rounded fp64 value.  M == 0 is a no-op.
+ * FRT_ROPE_SCALE_PARTS (the three are ignored otherwise).  One rounding to
+ * fp32 of a value that is itself off by a few 2^-53 of the angle (far
+ * positions next to a zero of cos or sin: more than a step of so small a
+ * number).  M == 0 is a no-op.
  */
 int frt_build_rope_table_scaled(int M, int rot, long P, double theta, int scaling, double factor,
                                 double orig_len, double low_turns, double high_turns,
@@ -553,7 +555,8 @@ typedef struct frt_qk_rope_desc {
 
 /*
  * frt_qk_norm_rope: for every token and every q and k head x of its row,
- * in fp32 (the mean square summed in fp64),
+ * in fp32 (the mean square summed in fp64 and rounded to fp32: past fp32's
+ * range it is infinite, and the head 0),
  *   y = x / sqrt(mean(x^2) + eps) * norm      (q_norm / k_norm; NULL: y = x)
  *   the first `rot` elements rotated in pairs (x0, x1) by the table's
  *   (c, s): (x0 c - x1 s, x0 s + x1 c); the others kept; rounded once to bf16
@@ -577,8 +580,9 @@ int frt_qk_norm_rope(const frt_qk_rope_desc* d, void* stream);
  * (1 / k_scale) (v_scale for v; the reciprocal and the product rounded to
  * fp32), scale = e4m3(min(max|y| / 6, 448)), code = e2m1(y / scale), both
  * nearest-even and saturating; scale 0 gives codes 0.  A NaN element counts
- * as 0 in max|y| and its code is a finite one.  k_out and v_out are ignored.  The slots
- * of one call must be distinct (two tokens in one slot leave a mix of both).
+ * as 0 in max|y| and its code is a finite one.  A zero keeps its sign.  k_out
+ * and v_out are ignored.  The slots of one call must be distinct (two tokens
+ * in one slot leave a mix of both).
  * A slot >= n_pages * page_size is not written, and the status word records
  * FRT_ERANGE; a bad position leaves the whole token out, as above.
  * hkv >= 1; hd % 16 == 0 for FRT_PAGE_E2M1.
@@ -615,7 +619,10 @@ typedef struct frt_paged_attn_desc {
 } frt_paged_attn_desc;
 
 /* Workspace bytes frt_paged_attention_fp4 needs (current device); they
- * depend on n_seqs, max_q, the heads and hd only, not on the lengths. */
+ * depend on n_seqs, max_q, the heads and hd only, not on the lengths.  Fewer
+ * or shorter sequences may need more (idle SMs share out the keys, 0 bytes
+ * where there are none): a workspace for several shapes has the largest of
+ * their sizes, not the size of the largest. */
 size_t frt_paged_attention_workspace_size(int n_seqs, int max_q, int hq, int hkv, int hd);
 
 /*
@@ -626,11 +633,15 @@ size_t frt_paged_attention_workspace_size(int n_seqs, int max_q, int hq, int hkv
  * sees keys j <= p, with window > 0 also j > p - window, else all keys.
  *   out = sum_j softmax_j(sm_scale * q . k_j) v_j,  lse = log sum exp
  * (natural logarithm); query head h reads kv head h / (hq / hkv).  A row that
- * sees no key gives out = 0 and lse = -inf.  Rows outside every sequence keep
- * what they held.  Products on the tensor cores with fp32 sums: the cached
- * codes times their block scales are exact in fp16, q is scaled by a power
- * of two into it, the weights are rounded to fp16 once; softmax statistics
- * and sums in fp32; results are the same from call to call.
+ * sees no key gives out = 0 and lse = -inf; a NaN in q makes its row and head
+ * NaN, out and lse.  Rows outside every sequence keep what they held.
+ * Products on the tensor cores with fp32 sums: the cached codes times their
+ * block scales are exact in fp16, q is scaled by a power of two into it, the
+ * weights are rounded to fp16 once (about one output in ten then lies a bf16
+ * step from that of fp32 weights); softmax statistics and sums in fp32;
+ * results are the same from call to call.  Scores and the product of the two
+ * scales must stay within fp32's range; the scales of cached tokens are
+ * finite (frt_paged_kv_append writes no other).
  * Sequences of very different query counts are better called apart: every
  * sequence is scheduled like one of max_q rows, of which a short one's share
  * ends at once.
@@ -638,6 +649,8 @@ size_t frt_paged_attention_workspace_size(int n_seqs, int max_q, int hq, int hkv
  * leaves its counters at zero.  Calls (and captured graphs) that share one
  * must not overlap.  Only the pages that hold a sequence's first kv_len
  * tokens are read; what the last page holds behind them does not matter.
+ * With a window, pages before every query's window may be looked up as far as
+ * they share 128 keys with one: keep a page of this pool in their place.
  * Device-side data that is out of range is never followed: a page id outside
  * [0, n_pages) hides its tokens, kv_len is held to [0, max_pages *
  * page_size], a sequence's rows to [0, rows] and its first max_q; each of
