@@ -16,6 +16,10 @@ constexpr float kLn2 = 0.6931471805599453f;
 // hidden score (-inf) stays hidden: where the scale, or its product with the
 // row's power of two, is below it, scores are within 2^-100 of 0 either way.
 constexpr float kLeastFactor = 1.17549435e-38f;
+__device__ __forceinline__ float score_factor(float scale, float up) {
+  const float f = fabsf(scale) * up;
+  return f < kLeastFactor ? kLeastFactor : f;   // a NaN stays
+}
 // the running maximum of a row that has seen no key: below every score, and
 // finite, so that a hidden score's distance to it is -inf
 constexpr float kNoKey = -3.402823466e38f;

@@ -336,7 +336,6 @@ attn_few_kernel(AttnArgs a) {
   // the sign of the scale goes into Q, so that the largest score is that of
   // the largest product
   const float scale = *a.k_scale * a.sm_scale * kLog2e;
-  auto factor_of = [&](float up) { return fmaxf(up * fabsf(scale), kLeastFactor); };
   const float vscale = *a.v_scale;
   // where in a stage this lane's bytes of the warp's first group lie, and
   // the way to the next group (in the next record's piece, if that is 16 keys)
@@ -414,7 +413,7 @@ attn_few_kernel(AttnArgs a) {
       } else {
 #pragma unroll
         for (int e2 = 0; e2 < 2; ++e2)
-          cq[nt][e2] = factor_of(__shfl_sync(0xffffffffu, up, (2 * t + e2) * 4));
+          cq[nt][e2] = score_factor(scale, __shfl_sync(0xffffffffu, up, (2 * t + e2) * 4));
       }
     }
     if constexpr (!C::kQRegs) {
@@ -422,7 +421,7 @@ attn_few_kernel(AttnArgs a) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e2 = 0; e2 < 2; ++e2) cq[nt][e2] = factor_of(join_m[nt * 8 + 2 * t + e2]);
+        for (int e2 = 0; e2 < 2; ++e2) cq[nt][e2] = score_factor(scale, join_m[nt * 8 + 2 * t + e2]);
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -552,7 +551,7 @@ attn_few_kernel(AttnArgs a) {
 #pragma unroll
               for (int e2 = 0; e2 < 2; ++e2) {
                 const float v = C::kQRegs ? true_cq[C::kQRegs ? nt : 0][e2]
-                                          : factor_of(join_m[nt * 8 + 2 * t + e2]);
+                                          : score_factor(scale, join_m[nt * 8 + 2 * t + e2]);
                 const float f = is_far<HD>(v) ? v : 1.0f;
 #pragma unroll
                 for (int u = 0; u < GR; ++u) {

@@ -305,7 +305,7 @@ attn_many_kernel(AttnArgs a, int splits, int tiles_max) {
     // the sign of the scale goes into Q, so that the largest score is that of
     // the largest product
     const float down = copysignf(__uint_as_float(uint32_t(254 - e) << 23), scale);
-    const float factor = fmaxf(fabsf(scale) * __uint_as_float(uint32_t(e) << 23), kLeastFactor);
+    const float factor = score_factor(scale, __uint_as_float(uint32_t(e) << 23));
 #pragma unroll 4
     for (int i = 0; i < HD / 8; ++i) {
       float f[8];
@@ -432,7 +432,7 @@ attn_many_kernel(AttnArgs a, int splits, int tiles_max) {
       mbar_arrive(&p_full[slot]);
     }
     };
-    if (__any_sync(0xffffffffu, c != factor)) attend(std::true_type{});
+    if (__any_sync(0xffffffffu, live && is_far<HD>(factor))) attend(std::true_type{});
     else attend(std::false_type{});
 
     // --- the row's result: through shared memory (after `done` every buffer

@@ -295,3 +295,16 @@ def test_keys_past_32_bits(rt):  # noqa: F811
                 want = ref.E2M1[codes] * np.repeat(ref.E4M3[s8], 16, -1) * 0.25
             assert np.array_equal(bf16_value(runtime.bf16_host(kv[i])).reshape(want.shape), want)
         del pool
+
+
+@pytest.mark.parametrize("Lq", [1, 3, 60])
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("which", ["k_scale", "v_scale"])
+def test_scales_of_nan(rt, Lq, hd, which):  # noqa: F811
+    """A page scale that is NaN is not taken for a scale of nothing."""
+    torch = rt[2]
+    p = Problem(rt, np.random.default_rng(43), [(Lq, 150), (1, 70)], 4, 2, hd, 16)
+    p.t[which].fill_(float("nan"))
+    p.run()
+    assert bool(torch.isnan(p.out[:p.cu[-1], :4 * hd]).all())
+    assert bool(torch.isnan(p.lse[:p.cu[-1]]).all()) == (which == "k_scale")
