@@ -7,7 +7,7 @@ import pytest
 
 import paged_ref as ref
 from fp8_transformer_block_b200.synth import bf16_bits, bf16_value
-from test_gpu_paged import page_fields, record_rows
+from test_gpu_paged import check_rows, page_fields, record_rows, run_heads
 from test_gpu_paged_attention import Problem, rt  # noqa: F401  (rt: the fixture)
 
 pytestmark = pytest.mark.gpu
@@ -308,3 +308,85 @@ def test_scales_of_nan(rt, Lq, hd, which):  # noqa: F811
     p.run()
     assert bool(torch.isnan(p.out[:p.cu[-1], :4 * hd]).all())
     assert bool(torch.isnan(p.lse[:p.cu[-1]]).all()) == (which == "k_scale")
+
+
+@pytest.mark.parametrize("rows", [5, 2500])
+@pytest.mark.parametrize("fmt", [0, 1])
+def test_heads_without_positions_or_q(rt, rows, fmt):  # noqa: F811
+    """positions NULL: 0, 1, 2, ...; an append with q_out NULL writes the
+    same pages and no q; a NULL k_out or v_out is left out of a read."""
+    frt, runtime, torch = rt
+    case = (rows, 6, 2, 64, 32, True, True, 0)
+    d, keep, q, k, _, xv = run_heads(rt, np.random.default_rng(44), *case)
+    keep[2].copy_(torch.arange(rows, dtype=torch.int32))
+    f, slots, pool, kv, keep2 = page_fields(rt, fmt, np.random.default_rng(45), rows, 2, 64, 16)
+    for key, val in f.items():
+        setattr(d, key, frt.ptr(val) if hasattr(val, "data_ptr") else val)
+    frt.frt_qk_norm_rope(d)
+    frt.frt_paged_kv_append(d)
+    torch.cuda.synchronize()
+    want = q.clone(), k.clone(), pool.clone()
+    tab, pos = keep[1].cpu().numpy(), np.arange(rows)
+    w = [bf16_value(runtime.bf16_host(t)).astype(np.float64) for t in keep[3:5]]
+    check_rows(runtime, q, rows, 6, 64, ref.norm_rotate(xv[:, :6], w[0], 1e-6, tab, pos, 32, True))
+    check_rows(runtime, k, rows, 2, 64, ref.norm_rotate(xv[:, 6:8], w[1], 1e-6, tab, pos, 32, True))
+    d.positions = None
+    for t in (q, k):
+        t.fill_(3.0)
+    pool.fill_(0xA5)
+    frt.frt_qk_norm_rope(d)
+    frt.frt_paged_kv_append(d)
+    torch.cuda.synchronize()
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1]) and torch.equal(pool, want[2])
+    q.fill_(3.0)
+    pool.fill_(0xA5)
+    d.q_out = None
+    frt.frt_paged_kv_append(d)
+    torch.cuda.synchronize()
+    assert bool((q == 3).all()) and torch.equal(pool, want[2])
+    got = []
+    for ko, vo in ((0, 1), (0, None), (None, 1)):
+        for t in kv:
+            t.fill_(3.0)
+        d.k_out, d.ld_k = None if ko is None else frt.ptr(kv[0]), 128
+        d.v_out, d.ld_v = None if vo is None else frt.ptr(kv[1]), 128
+        frt.frt_paged_kv_read(d)
+        torch.cuda.synchronize()
+        got.append([t.clone() for t in kv])
+    assert torch.equal(got[0][0], got[1][0]) and bool((got[1][1] == 3).all())
+    assert torch.equal(got[0][1], got[2][1]) and bool((got[2][0] == 3).all())
+    assert not bool((got[0][0] == 3).all()) and frt.frt_device_status(True) == frt.FRT_OK
+
+
+@pytest.mark.parametrize("a,b", [(1, 1), (1, 60), (60, 60)])
+def test_two_calls_at_once(rt, a, b):  # noqa: F811
+    """Two streams, a workspace each, in turn and captured: the same bits as
+    alone."""
+    frt, runtime, torch = rt
+    ps = [Problem(rt, np.random.default_rng(46 + i), [(n, 3000), (n, 700)], 8, 2, 128, 32) for i, n in enumerate((a, b))]
+    for p in ps:
+        p.run()
+        p.check()
+    want = [(p.out.clone(), p.lse.clone()) for p in ps]
+    streams = [torch.cuda.Stream() for _ in ps]
+    graphs = []
+    for p, s in zip(ps, streams):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            for _ in range(3):
+                frt.frt_paged_attention_fp4(p.d)
+        graphs.append(g)
+    for captured in (False, True):
+        for p in ps:
+            p.out.fill_(5.0)
+            p.lse.fill_(5.0)
+        torch.cuda.synchronize()
+        for _ in range(20):
+            for p, s, g in zip(ps, streams, graphs):
+                with torch.cuda.stream(s):
+                    g.replay() if captured else frt.frt_paged_attention_fp4(p.d)
+        torch.cuda.synchronize()
+        assert frt.frt_device_status(True) == frt.FRT_OK
+        for p, (out, lse) in zip(ps, want):
+            assert torch.equal(p.out, out) and torch.equal(p.lse, lse)
+            counters_are_zero(p)
