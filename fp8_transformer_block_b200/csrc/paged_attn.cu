@@ -110,7 +110,7 @@ __device__ __forceinline__ void lds(const uint8_t* p, uint32_t (&w)[BYTES / 4]) 
 // and the last of its CTAs to finish joins them in order.
 //
 // 61 sequences of one token and 700 to 16384 keys, 32 q heads on 8 of 128, run
-// in 133 us (93 for the bytes).  No unit is full: on 24 sequences of 8500 keys
+// in 133 to 138 us (93 for the bytes).  No unit is full: on 24 sequences of 8500 keys
 // 56 % of the issue slots and 3.6 TB/s.  The 12 computing warps of an SM have
 // a chain each from the widening (most of the 331 warp instructions for 16
 // keys of a kv head) over the products and the softmax to the next widening,
